@@ -14,11 +14,13 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
+from .decoder import (Attn, KvCache, Linear, Verifier, add_rmsnorm, kv_append, linear_q8, tree_attention, verify)
 from ._lib import ACT, KERNEL_CLASSES, MASK_MODE, PI_OK, WTYPE, FfnDesc, PiError, StackDump, _ptr, lib
 
 __all__ = ["Context", "Ffn", "PiError", "predict", "sparse_ffn", "layer", "layer_noalloc", "q4_dequant", "compact", "glue", "stack_run",
            "stack_run_dump", "stack_profile", "KERNEL_CLASSES",
-           "hot_first_order", "permute_rows", "lib"]
+           "hot_first_order", "permute_rows", "lib", "KvCache", "Attn", "Verifier", "Linear", "kv_append",
+           "tree_attention", "verify", "add_rmsnorm", "linear_q8"]
 
 
 class Context:

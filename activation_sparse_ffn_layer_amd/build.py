@@ -1,14 +1,17 @@
-"""Build libpi.so (HIP for gfx950) in-tree with hipcc."""
+"""Build libpi.so (HIP for gfx950) in-tree with hipcc: one object per source file, then a link."""
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpi.so")
-SOURCES = [os.path.join(CSRC, "pi_lib.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("pi_lib.hip", "pi_attn.hip", "pi_kv.hip", "pi_linear.hip", "pi_norm.hip",
+                                           "pi_verify.hip")]
 
 
 def hipcc() -> str:
@@ -18,16 +21,18 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def command(out: str = LIB):
-    return [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+def compile_command(source: str, obj: str):
+    return [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-c",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument",
-            "-I", os.path.join(ROOT, "include"), *SOURCES, "-o", out]
+            "-I", os.path.join(ROOT, "include"), source, "-o", obj]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
+def link_command(objs, out: str):
+    return [hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", out]
+
+
+def _run(cmd, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -36,6 +41,15 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out.strip():
         print(out, flush=True)
+
+
+def build(verbose: bool = False) -> str:
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+            list(pool.map(lambda so: _run(compile_command(*so), verbose), zip(SOURCES, objs)))
+        _run(link_command(objs, tmp), verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,595 @@
+// Attention of drafted trees over the paged cache (pi_tree_attention).
+//
+// A key/value head's query rows (N nodes x G heads of the group) are columns of the matrix
+// cores' 32x32x16 products. For a tile of keys, S^T = K Q^T leaves each lane 16 keys of one
+// query column, so the softmax's maximum and sum are over a lane's registers and one exchange
+// between the wave's halves; exp(S - max) is then, as it lies, the B operand of
+// O^T += V^T P^T, where V^T comes from row-major V by transposing LDS reads. The maximum and the
+// sum run along (one pass over the cache) and are held in fp32, as are S and O; P is rounded to
+// the cache's type for the second product (half a step of that type per weight, as large as the
+// rounding of the output itself).
+//
+// The keys of a sequence are one axis: its cached positions, then its N new nodes. The axis is
+// cut in chunks of whole tiles, equally long for all sequences, so that the chunks of all heads
+// fill the chip once; partial results (O, max, sum) are joined by k_attn_join.
+#include <algorithm>
+#include <new>
+
+#include "pi_kv.hpp"
+
+using namespace pi;
+
+struct pi_attn {
+  pi_ctx* ctx;
+  const pi_kv* kv;
+  int heads, max_batch, max_nodes;
+  float scale;
+  uint8_t* ws;
+  float* part;      // [slots][kv heads][rows][DP]
+  float* ml;        // [slots][kv heads][rows][2]: maximum (log2 domain) and sum
+};
+
+namespace {
+
+struct AttnDev {
+  KvDev c;
+  const uint8_t *q, *kn, *vn;
+  uint8_t* out;
+  const uint64_t* tree;
+  const int32_t* ctx_len;
+  float *part, *ml;
+  long long q_batch, q_node, q_head, kv_batch, kv_node, kv_head, out_batch, out_node, out_head;
+  int B, N, H, HK, G, D, R;  // R = N * G query rows of a key/value head
+  int slots, row_tiles;
+  float scale2;  // scale * log2(e)
+};
+
+template <typename T> struct Mm;
+template <> struct Mm<half_t> {
+  typedef half8_t v8;
+  // weights are carried times 2^14 (at most 16384), so that fp16 keeps its 11 bits down to 2^-28
+  // of the largest; below, a long cache's many small weights would round away together
+  static constexpr float SHIFT = 14.f;
+  static constexpr uint32_t EXP = 0x7C00u;
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Mm<bf16_t> {
+  typedef bf8_t v8;
+  static constexpr float SHIFT = 0.f;
+  static constexpr uint32_t EXP = 0x7F80u;
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
+
+// The other half's value of v (lane ^ 32).
+__device__ __forceinline__ float swap_max(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return fmaxf(u2f(p[0]), u2f(p[1]));
+}
+__device__ __forceinline__ float swap_add(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return u2f(p[0]) + u2f(p[1]);
+}
+
+// Where chunk `slot` lies: sequence b, its tiles [t0, t1), its number of chunks and the first
+// one's slot; false past the last chunk. Chunks are `c` tiles long, the least c that needs no
+// more than `slots` of them in all (slots >= B). Every wave works it out for itself.
+struct Chunk {
+  int b, t0, t1, count, first;
+};
+template <int KT>
+__device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o) {
+  const int lane = threadIdx.x % WAVE;
+  auto tiles = [&](int b) { return b < a.B ? (kv_len(a.c, a.ctx_len, b) + a.N + KT - 1) / KT : 0; };
+  const int mine = tiles(lane);  // the sequence of this lane; more than 64 are read again
+  auto sum = [&](int c) {
+    int n = lane < a.B ? (mine + c - 1) / c : 0;
+    for (int b = lane + WAVE; b < a.B; b += WAVE) n += (tiles(b) + c - 1) / c;
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
+    return n;
+  };
+  const int total = sum(1);
+  int c = max(1, (total + a.slots - 1) / a.slots);
+  while (c > 1 && sum(c) > a.slots) c += max(1, c >> 5);
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += WAVE) {
+    const int tl = b0 == 0 ? mine : tiles(b0 + lane);
+    const int n = (tl + c - 1) / c;
+    int incl = n;
+#pragma unroll
+    for (int s = 1; s < WAVE; s <<= 1) {
+      const int t = __shfl_up(incl, s, WAVE);
+      if (lane >= s) incl += t;
+    }
+    const uint64_t hit = __ballot(before + incl > slot);
+    if (hit != 0) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int first = before + __shfl(incl - n, l, WAVE);
+      const int tb = __shfl(tl, l, WAVE);
+      o->b = b0 + l;
+      o->first = first;
+      o->count = __shfl(n, l, WAVE);
+      o->t0 = (slot - first) * c;
+      o->t1 = min(tb, o->t0 + c);
+      return true;
+    }
+    before += __shfl(incl, WAVE - 1, WAVE);
+  }
+  return false;
+}
+
+// LDS of a workgroup: keys, then values, of one tile (two where tiles are shared by waves). A
+// row's pitch is past the power of two: 16 bytes for K, whose rows are read 16 bytes a lane, 32
+// bytes for V, whose transposing reads take 32 bytes from each of 4 rows.
+template <int DP> constexpr int k_pitch() { return DP * 2 + 16; }
+template <int DP> constexpr int v_pitch() { return DP * 2 + 32; }
+template <int DP, int WQ, int WK, int KB>
+constexpr size_t attn_lds() {
+  const size_t kt = 32 * KB * WK;
+  const size_t tile = kt * (k_pitch<DP>() + v_pitch<DP>()) * (WQ > 1 ? 2 : 1);
+  const size_t merge = WK > 1 ? (size_t)WQ * WK * 32 * (DP + 4) * 4 + (size_t)WQ * WK * 64 * 4 : 0;
+  return tile > merge ? tile : merge;
+}
+
+// WQ waves along the query rows (32 each), WK along a tile's keys (32 KB each). With WQ == 1 a
+// wave loads and reads its own keys only and the tile loop has no barrier.
+template <typename T, int DP, int WQ, int WK, int KB>
+__global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
+  constexpr int KW = 32 * KB, KT = KW * WK, NT = 64 * WQ * WK;
+  constexpr bool OWN = WQ == 1;                          // tiles private to a wave
+  constexpr int LPR = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // lanes that load one row
+  constexpr int LROWS = OWN ? KW : KT, LTHR = OWN ? 64 : NT;
+  constexpr int RPP = LTHR / LPR, PASS = LROWS / RPP;
+  static_assert(PASS >= 1 && LROWS % RPP == 0, "a tile is whole passes");
+  constexpr int KS = DP / 16, DB = DP / 32;
+  constexpr int KP = k_pitch<DP>(), VP = v_pitch<DP>();
+  typedef typename Mm<T>::v8 v8;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int s_odd;  // a new node's value row holds an infinity or a NaN
+  const int pair = blockIdx.x % (a.slots * a.HK), rt = blockIdx.x / (a.slots * a.HK);
+  const int hk = pair % a.HK, slot = pair / a.HK;
+  Chunk ch;
+  if (!find_chunk<KT>(a, slot, &ch)) return;
+  if (threadIdx.x == 0) s_odd = 0;
+  __syncthreads();
+  const int b = ch.b;
+  const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, half = lane >> 5, l32 = lane & 31;
+  const int wq = wave / WK, wk = wave % WK;
+  const int len = kv_len(a.c, a.ctx_len, b), total = len + a.N;
+
+  // this lane's query row
+  const int row = (rt * WQ + wq) * 32 + l32;
+  const bool live = row < a.R;
+  const bool wave_live = (rt * WQ + wq) * 32 < a.R;
+  const int node = live ? row / a.G : 0, head = hk * a.G + (live ? row % a.G : 0);
+  v8 qf[KS];
+  {
+    const uint8_t* qp = a.q + 2 * ((long long)b * a.q_batch + (long long)node * a.q_node + (long long)head * a.q_head);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = 16 * s + 8 * half;
+      qf[s] = __builtin_bit_cast(v8, ld16_or0(qp + 2 * (d < a.D ? d : 0), live && d < a.D));
+    }
+  }
+  uint64_t seen = a.tree != nullptr ? a.tree[(long long)b * a.N + node] : (2ull << node) - 1;
+  if (a.N < 64) seen &= (1ull << a.N) - 1;
+
+  // loading: pass i of a thread is row lr + i * RPP of the tile (of the wave's part), piece lc
+  const int lt = OWN ? lane : (int)threadIdx.x;
+  const int lr = lt / LPR + (OWN ? wk * KW : 0), lc = lt % LPR;
+  const bool piece_in = lc * 8 < a.D;
+  uint8_t* const ks = smem + (OWN ? wk * KW * (KP + VP) : 0);
+  const long long khead = (long long)hk * a.c.head_stride, nhead = (long long)hk * a.kv_head + (long long)b * a.kv_batch;
+  u32x4 kr[PASS], vr[PASS];
+  auto load = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int p = tile * KT + lr + i * RPP;
+      const uint8_t *kp = a.kn, *vp = a.vn;
+      bool ok = piece_in && p < total;
+      long long at = 0;
+      if (p < len) {
+        uint32_t off;
+        const int page = kv_page(a.c, b, page_of(a.c.div, (uint32_t)p, &off));
+        ok = ok && page >= 0;
+        at = (long long)page * a.c.page_stride + (long long)off * a.c.token_stride + khead;
+        kp = static_cast<const uint8_t*>(a.c.k);
+        vp = static_cast<const uint8_t*>(a.c.v);
+      } else {
+        at = (long long)(p - len) * a.kv_node + nhead;
+      }
+      at = ok ? at + lc * 8 : 0;
+      kr[i] = ld16_or0(kp + 2 * at, ok);
+      vr[i] = ld16_or0(vp + 2 * at, ok);
+    }
+  };
+  // a stage is K rows, then V rows
+  constexpr int STAGE = LROWS * (KP + VP);
+  auto store = [&](int tile, int stage) {
+    uint8_t* base = ks + stage * STAGE;
+    if (tile * KT + KT > len) {
+      // A weight of zero times an infinity or a NaN is a NaN: such elements of the new nodes, whom
+      // not every row sees, stay out of the product and are added to the rows that see them at
+      // the end (every row sees the cached positions, where nothing has to be done).
+#pragma unroll
+      for (int i = 0; i < PASS; ++i)
+        if (tile * KT + lr + i * RPP >= len) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = vr[i][e];
+            const uint32_t lo = (w & Mm<T>::EXP) == Mm<T>::EXP ? 0xFFFFu : 0u;
+            const uint32_t hi = (w & (Mm<T>::EXP << 16)) == Mm<T>::EXP << 16 ? 0xFFFF0000u : 0u;
+            if (lo | hi) s_odd = 1;
+            vr[i][e] = w & ~(lo | hi);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int r = lt / LPR + i * RPP;
+      if (DP / 8 == LPR || lc < DP / 8) {
+        *reinterpret_cast<u32x4*>(base + r * KP + lc * 16) = kr[i];
+        *reinterpret_cast<u32x4*>(base + LROWS * KP + r * VP + lc * 16) = vr[i];
+      }
+    }
+  };
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i) o[i] = (f32x16){};
+  float m = -__builtin_inff(), l = 0.f;  // running maximum (log2 domain); this half's sum
+
+  auto compute = [&](int tile, int stage) {
+    const uint8_t* kb0 = ks + stage * STAGE + (OWN ? 0 : wk * KW) * KP;
+    const uint8_t* vb0 = ks + stage * STAGE + LROWS * KP + (OWN ? 0 : wk * KW) * VP;
+    f32x16 s[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      s[kb] = (f32x16){};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const v8 kf = __builtin_bit_cast(v8, ld16(kb0 + (kb * 32 + l32) * KP + 32 * i + 16 * half));
+        s[kb] = Mm<T>::mfma(kf, qf[i], s[kb]);
+      }
+    }
+    const int p0 = tile * KT + wk * KW;
+    if (p0 + KW > len) {  // the tile reaches the new nodes or the end
+      // Masked as bit operations: with a select on `position < len || bit`, the compiler put the
+      // -inf of the untaken side over the accumulators of lanes that keep theirs.
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int j0 = p0 + kb * 32 - len;  // the node of the block's first key
+        uint32_t vis = j0 >= 64 ? 0u : (uint32_t)(seen >> (j0 & 63));
+        if (j0 < 0) vis = j0 <= -32 ? ~0u : (uint32_t)(seen << -j0) | ((1u << -j0) - 1);
+        vis >>= 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[kb][r] = bfi_sel(0u - ((vis >> acc_row(r, 0)) & 1u), s[kb][r], -__builtin_inff());
+      }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
+    top = swap_max(top) * a.scale2;
+    const float mn = fmaxf(m, top);
+    const float base = mn == -__builtin_inff() ? 0.f : mn;  // nothing seen so far: weights 0
+    if (__any(mn > m)) {
+      const float f = __builtin_amdgcn_exp2f(m - base);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] *= f;
+    }
+    m = mn;
+    v8 pf[KB][2];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], a.scale2, Mm<T>::SHIFT - base));
+        l += w;
+        pf[kb][r >> 3][r & 7] = (T)w;
+      }
+    // V^T operand: 4 keys x 16 columns from each group of 16 lanes; a lane's 8 keys of the
+    // product are the 8 it holds weights of, 4 half + {0..3} and 8 + 4 half + {0..3}
+    const uint8_t* vl = vb0 + (4 * half + ((lane & 15) >> 2)) * VP + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          typedef __attribute__((address_space(3))) short4_t* lds4;
+          const uint8_t* p = vl + (kb * 32 + st * 16) * VP + 64 * i;
+          struct { short4_t x, y; } v;
+          v.x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+          v.y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 8 * VP));
+          o[i] = Mm<T>::mfma(__builtin_bit_cast(v8, v), pf[kb][st], o[i]);
+        }
+  };
+
+  if constexpr (OWN) {
+    load(ch.t0);
+    for (int t = ch.t0; t < ch.t1; ++t) {
+      store(t, 0);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (t + 1 < ch.t1) load(t + 1);
+      compute(t, 0);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  } else {
+    load(ch.t0);
+    store(ch.t0, 0);
+    if (ch.t0 + 1 < ch.t1) load(ch.t0 + 1);
+    __syncthreads();
+    for (int t = ch.t0; t < ch.t1; ++t) {
+      const int st = (t - ch.t0) & 1;
+      if (wave_live) compute(t, st);
+      if (t + 1 < ch.t1) store(t + 1, st ^ 1);
+      if (t + 2 < ch.t1) load(t + 2);
+      __syncthreads();
+    }
+  }
+
+  l = swap_add(l);
+  // 4 columns d..d+3 of a query row: the output itself when the sequence is one chunk
+  auto put = [&](int r, int d, f32x4 v, float mm, float ll) {
+    if (d >= a.D) return;
+    if (s_odd) {
+      const int rn = r / a.G;
+      uint64_t w = a.tree != nullptr ? a.tree[(long long)b * a.N + rn] : (2ull << rn) - 1;
+      for (int j = 0; j < a.N; ++j)
+        if (((w >> j) & 1) && len + j >= ch.t0 * KT && len + j < ch.t1 * KT) {
+          const T* x = reinterpret_cast<const T*>(a.vn) + nhead + (long long)j * a.kv_node + d;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float y = (float)x[i];
+            if (!(fabsf(y) < __builtin_inff())) v[i] += y;
+          }
+        }
+    }
+    if (ch.count == 1) {
+      const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+      T* o4 = reinterpret_cast<T*>(a.out) + (long long)b * a.out_batch + (long long)(r / a.G) * a.out_node +
+              (long long)(hk * a.G + r % a.G) * a.out_head + d;
+      struct __attribute__((aligned(8))) { T e[4]; } w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.e[i] = (T)(ll == 0.f ? 0.f : v[i] * inv);
+      __builtin_memcpy(__builtin_assume_aligned(o4, 8), &w, 8);
+    } else {
+      const long long at = ((long long)slot * a.HK + hk) * a.R + r;
+      *reinterpret_cast<f32x4*>(a.part + at * DP + d) = v;
+      if (d == 0) {
+        a.ml[2 * at] = mm;
+        a.ml[2 * at + 1] = ll;
+      }
+    }
+  };
+  if constexpr (WK == 1) {
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        put(row, 32 * i + acc_row(r, half), (f32x4){o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]}, m, l);
+  } else {
+    // join the WK waves of the same rows through LDS
+    constexpr int OP = DP + 4;
+    float* ob = reinterpret_cast<float*>(smem);              // [WQ][WK][32][OP]
+    float* mlb = ob + WQ * WK * 32 * OP;                     // [WQ][WK][32][2]
+    __syncthreads();  // the tiles are free
+    if (half == 0) {
+      mlb[(wave * 32 + l32) * 2] = m;
+      mlb[(wave * 32 + l32) * 2 + 1] = l;
+    }
+    __syncthreads();
+    float mt = -__builtin_inff(), ltot = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) mt = fmaxf(mt, mlb[((wq * WK + w) * 32 + l32) * 2]);
+    const float mb = mt == -__builtin_inff() ? 0.f : mt;
+    const float f = __builtin_amdgcn_exp2f(m - mb);
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<f32x4*>(ob + (wave * 32 + l32) * OP + 32 * i + acc_row(r, half)) =
+            (f32x4){o[i][r] * f, o[i][r + 1] * f, o[i][r + 2] * f, o[i][r + 3] * f};
+    __syncthreads();
+    constexpr int QP = DP / 4;  // quads of a row
+    for (int i = wk * WAVE + lane; i < 32 * QP; i += WK * WAVE) {
+      const int c = i / QP, d = 4 * (i % QP), r = (rt * WQ + wq) * 32 + c;
+      if (r >= a.R) break;
+      mt = -__builtin_inff();
+#pragma unroll
+      for (int w = 0; w < WK; ++w) mt = fmaxf(mt, mlb[((wq * WK + w) * 32 + c) * 2]);
+      const float mb2 = mt == -__builtin_inff() ? 0.f : mt;
+      ltot = 0.f;
+      f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        ltot += mlb[((wq * WK + w) * 32 + c) * 2 + 1] * __builtin_amdgcn_exp2f(mlb[((wq * WK + w) * 32 + c) * 2] - mb2);
+        v += *reinterpret_cast<const f32x4*>(ob + ((wq * WK + w) * 32 + c) * OP + d);
+      }
+      put(r, d, v, mt, ltot);
+    }
+  }
+}
+
+// out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over a sequence's chunks s, one wave per
+// query row, 4 columns per lane; rows of sequences of one chunk are done already.
+template <typename T, int DP, int KT>
+__global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
+  const int lane = threadIdx.x % WAVE;
+  // (b, hk, r) of this wave
+  const int id = blockIdx.x * NWAVES + threadIdx.x / WAVE;
+  if (id >= rows) return;
+  const int r = id % a.R, hk = id / a.R % a.HK, b = id / a.R / a.HK;
+  // the first slot of sequence b: the chunks before it
+  auto tiles = [&](int i) { return i < a.B ? (kv_len(a.c, a.ctx_len, i) + a.N + KT - 1) / KT : 0; };
+  auto sum = [&](int c, int end) {
+    int n = 0;
+    for (int i = lane; i < end; i += WAVE) n += (tiles(i) + c - 1) / c;
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
+    return n;
+  };
+  const int total = sum(1, a.B);
+  int c = max(1, (total + a.slots - 1) / a.slots);
+  while (c > 1 && sum(c, a.B) > a.slots) c += max(1, c >> 5);
+  const int first = sum(c, b), count = (tiles(b) + c - 1) / c;
+  if (count == 1) return;
+  float m = -__builtin_inff();
+  for (int s = lane; s < count; s += WAVE) m = fmaxf(m, a.ml[2 * ((((long long)first + s) * a.HK + hk) * a.R + r)]);
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, WAVE));
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  const int d = 4 * lane;
+  for (int s = 0; s < count; ++s) {
+    const long long at = (((long long)first + s) * a.HK + hk) * a.R + r;
+    const float f = __builtin_amdgcn_exp2f(a.ml[2 * at] - base);
+    l += a.ml[2 * at + 1] * f;
+    if (d < a.D) v += *reinterpret_cast<const f32x4*>(a.part + at * DP + d) * f;
+  }
+  if (d >= a.D) return;
+  T* o = reinterpret_cast<T*>(a.out) + (long long)b * a.out_batch + (long long)(r / a.G) * a.out_node +
+         (long long)(hk * a.G + r % a.G) * a.out_head + d;
+  struct __attribute__((aligned(8))) { T e[4]; } w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.e[i] = (T)(l == 0.f ? 0.f : v[i] / l);
+  __builtin_memcpy(__builtin_assume_aligned(o, 8), &w, 8);
+}
+
+// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences).
+struct AttnPlan {
+  int wq, row_tiles, slots;
+};
+AttnPlan attn_plan(int cus, int HK, int rows, int B) {
+  AttnPlan p;
+  p.wq = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
+  p.row_tiles = (rows + 32 * p.wq - 1) / (32 * p.wq);
+  const int wgs = p.wq == 8 ? cus : 2 * cus;  // workgroups the chip holds at once
+  p.slots = std::max(B, wgs / (HK * p.row_tiles));
+  return p;
+}
+constexpr int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+
+template <typename T, int DP, int WQ, int WK, int KB>
+pi_status launch_attn_t(pi_ctx* c, const AttnDev& a) {
+  constexpr size_t lds = attn_lds<DP, WQ, WK, KB>();
+  auto kern = k_tree_attn<T, DP, WQ, WK, KB>;
+  PI_HIP(c, allow_lds(kern, lds));
+  PI_HIP(c, launch_kb(c, 0, kern, dim3((unsigned)(a.slots * a.HK * a.row_tiles)), 64 * WQ * WK, lds, a));
+  if (a.slots > a.B) {
+    const int rows = a.B * a.HK * a.R;
+    PI_HIP(c, launch_k(c, 0, k_attn_join<T, DP, 32 * KB * WK>, dim3((rows + NWAVES - 1) / NWAVES), 0, a, rows));
+  }
+  return PI_OK;
+}
+
+template <typename T, int DP>
+pi_status launch_attn_d(pi_ctx* c, const AttnDev& a, int wq) {
+  constexpr int KB = DP <= 128 ? 2 : 1;
+  switch (wq) {
+    case 1: return launch_attn_t<T, DP, 1, 4, 1>(c, a);
+    case 2: return launch_attn_t<T, DP, 2, 2, 1>(c, a);
+    case 4: return launch_attn_t<T, DP, 4, 1, KB>(c, a);
+    default: return launch_attn_t<T, DP, 8, 1, KB>(c, a);
+  }
+}
+
+template <typename T>
+pi_status launch_attn(pi_ctx* c, const AttnDev& a, int wq) {
+  switch (padded_dim(a.D)) {
+    case 64: return launch_attn_d<T, 64>(c, a, wq);
+    case 96: return launch_attn_d<T, 96>(c, a, wq);
+    case 128: return launch_attn_d<T, 128>(c, a, wq);
+    default: return launch_attn_d<T, 256>(c, a, wq);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t max_batch, int32_t max_nodes, float scale,
+                         pi_attn** out) {
+  if (ctx == nullptr || out == nullptr) return PI_ERR_INVALID;
+  *out = nullptr;
+  if (kv == nullptr) return fail(ctx, PI_ERR_INVALID, "kv is NULL");
+  if (kv->ctx != ctx) return fail(ctx, PI_ERR_INVALID, "the cache belongs to another context");
+  if (heads < 1 || heads % kv->desc.heads)
+    return fail(ctx, PI_ERR_INVALID, "%d query heads are no multiple of the cache's %d", heads, kv->desc.heads);
+  if (max_batch < 1 || max_nodes < 1) return fail(ctx, PI_ERR_INVALID, "bad limits: %d sequences, %d nodes", max_batch, max_nodes);
+  if (max_nodes > 64) return fail(ctx, PI_ERR_UNSUPPORTED, "%d nodes: a tree has at most 64", max_nodes);
+  if (!(scale > 0.f) || scale > 3e38f) return fail(ctx, PI_ERR_INVALID, "scale must be finite and above 0");
+  const int HK = kv->desc.heads, G = heads / HK, DP = padded_dim(kv->desc.head_dim);
+  if ((int64_t)max_batch * max_nodes * heads >= (1ll << 31) / 64)
+    return fail(ctx, PI_ERR_UNSUPPORTED, "%d sequences of %d nodes and %d heads are too many", max_batch, max_nodes, heads);
+  // scratch of the largest call: rows (all heads, all slots) of any number of nodes and sequences
+  size_t rows = 0;
+  for (int n = 1; n <= max_nodes; ++n) {
+    const AttnPlan p = attn_plan(ctx->cus, HK, n * G, max_batch);
+    rows = std::max(rows, (size_t)p.slots * HK * n * G);
+  }
+  PI_HIP(ctx, hipSetDevice(ctx->device));
+  uint8_t* ws = nullptr;
+  const size_t ob = rows * DP * 4, mb = rows * 2 * 4;
+  if (hipMalloc(reinterpret_cast<void**>(&ws), ob + mb) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(ctx, PI_ERR_OOM, "attention scratch of %zu bytes", ob + mb);
+  }
+  pi_attn* a = new (std::nothrow) pi_attn{ctx, kv, heads, max_batch, max_nodes, scale, ws, reinterpret_cast<float*>(ws),
+                                          reinterpret_cast<float*>(ws + ob)};
+  if (a == nullptr) {
+    (void)hipFree(ws);
+    return fail(ctx, PI_ERR_OOM, "host allocation failed");
+  }
+  *out = a;
+  return PI_OK;
+}
+
+void pi_attn_destroy(pi_attn* attn) {
+  if (attn == nullptr) return;
+  (void)hipSetDevice(attn->ctx->device);
+  (void)hipFree(attn->ws);
+  delete attn;
+}
+
+pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args) {
+  if (ctx == nullptr) return PI_ERR_INVALID;
+  if (attn == nullptr) return fail(ctx, PI_ERR_INVALID, "attn is NULL");
+  if (attn->ctx != ctx) return fail(ctx, PI_ERR_INVALID, "attn belongs to another context");
+  if (args == nullptr) return fail(ctx, PI_ERR_INVALID, "args is NULL");
+  const pi_attn_args& a = *args;
+  const pi_kv* kv = attn->kv;
+  PI_TRY(check_paging(ctx, kv, a.table, a.table_stride, a.table_width, a.ctx_len, a.B, a.N));
+  if (a.B > attn->max_batch || a.N > attn->max_nodes)
+    return fail(ctx, PI_ERR_INVALID, "B %d, N %d above the handle's %d, %d", a.B, a.N, attn->max_batch, attn->max_nodes);
+  PI_TRY(check_bnh(ctx, "q", a.q, a.q_batch, a.q_node, a.q_head));
+  PI_TRY(check_bnh(ctx, "k_new", a.k_new, a.kv_batch, a.kv_node, a.kv_head));
+  PI_TRY(check_bnh(ctx, "v_new", a.v_new, a.kv_batch, a.kv_node, a.kv_head));
+  PI_TRY(check_bnh(ctx, "out", a.out, a.out_batch, a.out_node, a.out_head));
+  if (reinterpret_cast<uintptr_t>(a.tree) & 7u) return fail(ctx, PI_ERR_INVALID, "tree is not 8-byte aligned");
+  PI_HIP(ctx, hipSetDevice(ctx->device));
+  const int HK = kv->desc.heads, G = attn->heads / HK;
+  const AttnPlan p = attn_plan(ctx->cus, HK, a.N * G, a.B);
+  const AttnDev d{kv_dev(kv, a.table, a.table_stride, a.table_width), static_cast<const uint8_t*>(a.q),
+                  static_cast<const uint8_t*>(a.k_new), static_cast<const uint8_t*>(a.v_new),
+                  static_cast<uint8_t*>(a.out), a.tree, a.ctx_len, attn->part, attn->ml, a.q_batch, a.q_node, a.q_head,
+                  a.kv_batch, a.kv_node, a.kv_head, a.out_batch, a.out_node, a.out_head, a.B, a.N, attn->heads, HK, G,
+                  kv->desc.head_dim, a.N * G, p.slots, p.row_tiles, attn->scale * 1.4426950408889634f};
+  return kv->desc.dtype == PI_T_F16 ? launch_attn<half_t>(ctx, d, p.wq) : launch_attn<bf16_t>(ctx, d, p.wq);
+}
+
+}  // extern "C"

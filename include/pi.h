@@ -282,6 +282,187 @@ pi_status pi_hot_first_order(const double *p, int32_t ffn, int32_t *perm);
 pi_status pi_permute_rows(pi_ctx *ctx, const void *src, void *dst, const int32_t *perm,
                           int32_t rows, int64_t row_bytes);
 
+/* ---------------------------------------------------------------- the decoder around the FFN
+ *
+ * The dense operators a decoder layer needs next to the sparse FFN when it serves drafted
+ * tokens: attention of a tree of tokens over a paged key/value cache, the append of the
+ * accepted tokens to that cache, the check of drafted tokens against the target's
+ * distribution, the residual's RMS norm with an 8-bit output, and the 8-bit matrix product.
+ * They follow the conventions above. Tensors of these calls may be views: strides are given
+ * in elements, the last axis is contiguous, and rows start at a multiple of 16 bytes unless a
+ * call says otherwise. A handle (pi_kv, pi_attn, pi_verifier, pi_linear) keeps its own scratch,
+ * sized when it is created, and borrows the pointers of its description. */
+
+typedef enum { PI_T_F32 = 0, PI_T_F16 = 1, PI_T_BF16 = 2 } pi_dtype;
+
+typedef struct pi_kv pi_kv;
+typedef struct pi_attn pi_attn;
+typedef struct pi_verifier pi_verifier;
+typedef struct pi_linear pi_linear;
+
+/* A key/value cache of one layer: `pages` pages of page_tokens tokens each, k and v alike.
+ * Token t of page p, head h is head_dim contiguous elements at p*page_stride + t*token_stride +
+ * h*head_stride.
+ *   dtype      PI_T_F16 or PI_T_BF16
+ *   heads      key/value heads; head_dim a multiple of 8 up to 256
+ *   strides    in elements, multiples of 8
+ * Which pages a sequence has is an argument of the calls: table, int32 [B][table_width] with
+ * table_stride elements between sequences, names page table[b][i] for the positions from
+ * i*page_tokens on. A NULL table stands for one page each, page b for sequence b. Positions
+ * are below table_width*page_tokens, which must be below 2^31 - 64. Tokens of a page number
+ * outside the cache count as zeros where they are read and are dropped where they are written. */
+typedef struct pi_kv_desc {
+  int32_t dtype;
+  int32_t heads, head_dim, pages, page_tokens;
+  void *k, *v;
+  int64_t page_stride, token_stride, head_stride;
+} pi_kv_desc;
+
+pi_status pi_kv_create(pi_ctx *ctx, const pi_kv_desc *desc, pi_kv **out);
+void pi_kv_destroy(pi_kv *kv);
+
+/* Append tokens to the cache: token nodes[b][j] (j itself when nodes is NULL) of sequence b's N
+ * new tokens goes to position ctx_len[b] + j, for j < n[b] (all N when n is NULL).
+ *   k_new, v_new  [B][N][heads][head_dim] of the cache's type, strides for both
+ *   ctx_len    device int32 [B]: tokens held before the call (negative: 0)
+ *   nodes, n   device int32 [B][N] and [B], nullable; an entry outside [0, N) writes nothing
+ *   len_out    device int32 [B], nullable: ctx_len + n, at most the table's positions. It may be
+ *              ctx_len itself.
+ * Positions beyond the table are dropped. Two sequences must not share the pages written. */
+typedef struct pi_append_args {
+  const void *k_new, *v_new;
+  int64_t kv_batch, kv_node, kv_head;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t *ctx_len;
+  const int32_t *nodes, *n;
+  int32_t *len_out;
+  int32_t B, N;
+} pi_append_args;
+
+pi_status pi_kv_append(pi_ctx *ctx, const pi_kv *kv, const pi_append_args *args);
+
+/* Attention of drafted trees over the cache. Node i of sequence b sees every cached position
+ * below ctx_len[b] and the new nodes j whose bit j is set in tree[b][i]:
+ *   out[b][i][h] = sum_p w_p v_p,  w = softmax over the seen p of scale * q[b][i][h] . k_p,
+ * with key/value head h * kv_heads / heads. A node that sees nothing gets zeros; what is not
+ * seen does not enter the result, whatever it holds.
+ *   heads      query heads, a multiple of the cache's heads
+ *   scale      finite, above 0
+ *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch */
+pi_status pi_attn_create(pi_ctx *ctx, const pi_kv *kv, int32_t heads, int32_t max_batch, int32_t max_nodes,
+                         float scale, pi_attn **out);
+void pi_attn_destroy(pi_attn *attn);
+
+/*   q, out     [B][N][heads][head_dim] of the cache's type
+ *   k_new, v_new  [B][N][kv heads][head_dim], the new nodes' keys and values (strides for both)
+ *   tree       device uint64 [B][N], or NULL: node i sees nodes 0..i (a chain)
+ *   ctx_len    device int32 [B], taken as 0 below 0 and as the table's positions above them */
+typedef struct pi_attn_args {
+  const void *q;
+  int64_t q_batch, q_node, q_head;
+  const void *k_new, *v_new;
+  int64_t kv_batch, kv_node, kv_head;
+  const uint64_t *tree;
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t *ctx_len;
+  void *out;
+  int64_t out_batch, out_node, out_head;
+  int32_t B, N;
+} pi_attn_args;
+
+pi_status pi_tree_attention(pi_ctx *ctx, pi_attn *attn, const pi_attn_args *args);
+
+/* Check of drafted tokens against the target's distribution by rejection sampling, so that the
+ * tokens kept are distributed as the target's own. Node 0 is the last token already kept; node
+ * i > 0 has parent parents[b][i] < i and token tokens[b][i]; logits[b][i] is the target's row
+ * after node i. With p = softmax(logits[cur] / temperature) (all weight on the lowest index of
+ * the largest logit where the temperature is not above 0), the children of the current node
+ * are tried in index order, starting from r = p:
+ *   with q:     child t is taken where u[b][i] * q[b][cur][t] < r[t]; else r becomes
+ *               max(r - q[b][cur], 0), normalised
+ *   without q:  child t is taken where u[b][i] < r[t]; else r[t] becomes 0 and r is normalised
+ * until a node has no child that is taken. The next token is then drawn from r (from p where r
+ * has no weight left) at u_next[b]: the first whose running sum is above u_next * the total.
+ * NaN logits count as -inf, +inf as the largest finite value; a row of nothing else but -inf
+ * gives the next token -1. Sums are in 64 bits and in a fixed order.
+ *   logits     [B][N][vocab], rows need no alignment beyond the element's
+ *   q          fp32 [B][N][vocab] or NULL: the draft's probabilities after each node
+ *   tokens, parents  device int32 [B][N]; a parent outside [0, i) keeps node i off every path
+ *   u, u_next, temperature  device fp32 [B][N], [B], [B] (NULL: 1)
+ *   nodes, out device int32 [B][N]: the path's nodes from node 0 on; their tokens without node
+ *              0's, then the next token; both filled up with -1
+ *   n          device int32 [B]: the path's length */
+pi_status pi_verifier_create(pi_ctx *ctx, int32_t vocab, int32_t max_batch, int32_t max_nodes, pi_verifier **out);
+void pi_verifier_destroy(pi_verifier *ver);
+
+typedef struct pi_verify_args {
+  const void *logits;
+  int32_t dtype;
+  int64_t logits_batch, logits_node;
+  const float *q;
+  int64_t q_batch, q_node;
+  const int32_t *tokens, *parents;
+  const float *u, *u_next, *temperature;
+  int32_t *nodes, *out, *n;
+  int32_t B, N;
+} pi_verify_args;
+
+pi_status pi_verify(pi_ctx *ctx, pi_verifier *ver, const pi_verify_args *args);
+
+/* The residual's addition and RMS norm, with the norm in 8 bits, for T rows of d:
+ *   res_out = round(x + res)            to res's type (x's, where res is NULL)
+ *   y       = res_out / sqrt(mean(res_out^2) + eps) * w      in fp32
+ *   scale   = max |y| / 127,  q = round(y / scale)           (0 and 0 for a row of zeros)
+ *   x, res, res_out  any pi_dtype (res_out has res's; it may be x or res itself)
+ *   w          fp32 [d]; d a multiple of 8 up to 32768
+ *   q, scale   int8 [T][d] (rows 8-byte aligned) and fp32 [T], both or neither
+ *   y          [T][d] of y_dtype, nullable
+ * Strides are between rows. */
+typedef struct pi_norm_args {
+  const void *x, *res;
+  void *res_out;
+  int32_t x_dtype, res_dtype;
+  int64_t x_stride, res_stride, res_out_stride;
+  const float *w;
+  float eps;
+  int8_t *q;
+  int64_t q_stride;
+  float *scale;
+  void *y;
+  int32_t y_dtype;
+  int64_t y_stride;
+  int32_t T, d;
+} pi_norm_args;
+
+pi_status pi_add_rmsnorm(pi_ctx *ctx, const pi_norm_args *args);
+
+/* A weight of N x K 8-bit integers with one scale per output channel.
+ *   w          int8 [N][K], w_stride elements between rows (a multiple of 16); K a multiple of
+ *              16 below 131072 (the sums are exact in 32 bits)
+ *   w_scale    fp32 [N]; bias fp32 [N] or NULL
+ *   max_tokens limit of M, which sizes the scratch */
+typedef struct pi_linear_desc {
+  int32_t N, K;
+  const int8_t *w;
+  int64_t w_stride;
+  const float *w_scale, *bias;
+  int32_t max_tokens;
+} pi_linear_desc;
+
+pi_status pi_linear_create(pi_ctx *ctx, const pi_linear_desc *desc, pi_linear **out);
+void pi_linear_destroy(pi_linear *lin);
+
+/* y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n] for M tokens, the sum in
+ * whole numbers.
+ *   x          int8 [M][K], x_stride a multiple of 16; x_scale fp32 [M]
+ *   y          [M][N] of y_dtype; rows need no alignment beyond the element's */
+pi_status pi_linear_q8(pi_ctx *ctx, pi_linear *lin, const int8_t *x, int64_t x_stride, const float *x_scale, int32_t M,
+                       void *y, int32_t y_dtype, int64_t y_stride);
+
 #ifdef __cplusplus
 }
 #endif
