@@ -28,18 +28,16 @@ struct LinDev {
 
 template <typename T> struct Vec4 { typedef T type __attribute__((ext_vector_type(4))); };
 
-// y[m][n0..n0+3] from 4 whole-number sums
+// y[m][n0..n0+3] from 4 whole-number sums and their channels' scales and biases
 template <typename T>
-__device__ __forceinline__ void put4(const LinDev& p, int m, int n0, i32x4 s, bool wide) {
+__device__ __forceinline__ void put4(const LinDev& p, int m, int n0, const float (&ws)[4], const float (&bias)[4], i32x4 s,
+                                     bool wide) {
   if (m >= p.M || n0 >= p.N) return;
   const float xs = p.xs[m];
   T* y = static_cast<T*>(p.y) + (long long)m * p.y_stride + n0;
   float v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = min(n0 + i, p.N - 1);
-    v[i] = (float)s[i] * xs * p.ws[n] + (p.bias != nullptr ? p.bias[n] : 0.f);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = (float)s[i] * xs * ws[i] + bias[i];
   if (wide && n0 + 3 < p.N) {
     typedef typename Vec4<T>::type V;
     V o;
@@ -51,6 +49,17 @@ __device__ __forceinline__ void put4(const LinDev& p, int m, int n0, i32x4 s, bo
     for (int i = 0; i < 4; ++i)
       if (n0 + i < p.N) y[i] = (T)v[i];
   }
+}
+template <typename T>
+__device__ __forceinline__ void put4(const LinDev& p, int m, int n0, i32x4 s, bool wide) {
+  float ws[4], bias[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = min(n0 + i, p.N - 1);
+    ws[i] = p.ws[n];
+    bias[i] = p.bias != nullptr ? p.bias[n] : 0.f;
+  }
+  put4<T>(p, m, n0, ws, bias, s, wide);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -117,83 +126,124 @@ __global__ __launch_bounds__(64 * LR_WAVES) void k_q8_rows(LinDev p, bool wide) 
 }
 
 // ---------------------------------------------------------------------------------------
-// Many tokens: bound by the matrix cores. A workgroup owns a tile of TN weight rows x TM
-// tokens, staged in LDS 128 bytes of K at a time (two stages: the next one's loads are in
-// flight during the products).
+// Many tokens: bound by the matrix cores. Four waves own a square tile of 64 FB weight rows and
+// tokens, staged in LDS 128 bytes of K at a time in two stages: during the products of one, the
+// other is written from registers and the registers are loaded anew, spread over the steps.
+// A wave's quarter of the tile is FB x FB blocks of 32 x 32, so LDS is read 2 FB rows for FB^2
+// products: with FB = 4 half as often per product as with 2, which LDS bandwidth bounds.
 // ---------------------------------------------------------------------------------------
 constexpr int LT_K = 128, LT_P = LT_K + 16;  // K bytes per stage; LDS row pitch (bytes)
+constexpr uint32_t LT_OOB = 0xC0000000u;     // past any tile's records: reads as zero
+template <int FB> constexpr size_t tile_lds() { return (size_t)2 * 2 * 64 * FB * LT_P; }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_q8_tile(LinDev p, bool wide) {
-  constexpr int TN = 128, TM = 128;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(TN + TM) * LT_P];
+// The tile of workgroup id: the XCDs (id % 8) take equal runs of tiles, in an order that
+// walks 8 tiles of tokens, then the weight rows, so that an XCD's tiles in flight share rows.
+__device__ __forceinline__ void tile_of(int id, int tn, int tm, int* n, int* m) {
+  const int total = tn * tm, x = id & 7, each = total >> 3, more = total & 7;
+  const int t = x * each + min(x, more) + (id >> 3);
+  const int group = t / (8 * tn), r = t - group * 8 * tn, high = min(8, tm - group * 8);
+  *m = group * 8 + r % high;
+  *n = r / high;
+}
+
+template <typename T, int FB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FB == 4 ? 1 : 2)))
+void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
+  constexpr int TL = 64 * FB, R = 4 * FB, STAGE = 2 * TL * LT_P;  // R loads of 32 rows for both operands
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, half = lane >> 5, l32 = lane & 31;
-  const int n0 = blockIdx.x * TN, m0 = blockIdx.y * TM;
+  int nt, mt;
+  tile_of(blockIdx.x, tn, tm, &nt, &mt);
+  const int n0 = nt * TL, m0 = mt * TL;
   const int lr = threadIdx.x >> 3, lk = 16 * (threadIdx.x & 7);  // row of a pass of 32, byte in the row
-  const int8_t* src[8];
+  const int wrows = min(TL, p.N - n0), xrows = min(TL, p.M - m0);
+  const auto wb = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p.w) + (long long)n0 * p.w_stride, (short)0,
+                                                    (int)((wrows - 1) * p.w_stride + p.K), 0x00020000);
+  const auto xb = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p.x) + (long long)m0 * p.x_stride, (short)0,
+                                                    (int)((xrows - 1) * p.x_stride + p.K), 0x00020000);
+  uint32_t at[R];  // rows past the last read it again
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    src[i] = p.w + (long long)min(n0 + lr + 32 * i, p.N - 1) * p.w_stride;
-    src[4 + i] = p.x + (long long)min(m0 + lr + 32 * i, p.M - 1) * p.x_stride;
+  for (int i = 0; i < R / 2; ++i) {
+    at[i] = (uint32_t)(min(lr + 32 * i, wrows - 1) * (int)p.w_stride + lk);
+    at[R / 2 + i] = (uint32_t)(min(lr + 32 * i, xrows - 1) * (int)p.x_stride + lk);
   }
-  u32x4 r[8];
-  auto load = [&](int k0) {
-    const bool in = k0 + lk < p.K;
-    const int k = in ? k0 + lk : 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = ld16_or0(src[i] + k, in);
+  u32x4 r[R];
+  auto load = [&](int i, int k0) {
+    const uint32_t o = k0 + lk < p.K ? at[i] + k0 : LT_OOB;
+    r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(i < R / 2 ? wb : xb, o, 0, 0));
   };
-  auto store = [&](int s) {
+  auto store = [&](int i, int s) { *reinterpret_cast<u32x4*>(lds + s * STAGE + (lr + 32 * i) * LT_P + lk) = r[i]; };
+  i32x16 acc[FB][FB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<u32x4*>(&lds[s][(lr + 32 * i) * LT_P + lk]) = r[i];
-  };
-  i32x16 acc[2][2];
+  for (int i = 0; i < FB; ++i)
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = (i32x16){};
-  const int wn = 64 * (wave & 1), wm = 64 * (wave >> 1);
+    for (int j = 0; j < FB; ++j) acc[i][j] = (i32x16){};
+  const int wn = 32 * FB * (wave & 1), wm = 32 * FB * (wave >> 1);
   const int steps = (p.K + LT_K - 1) / LT_K;
-  load(0);
-  store(0);
-  if (steps > 1) load(LT_K);
+#pragma unroll
+  for (int i = 0; i < R; ++i) load(i, 0);
+#pragma unroll
+  for (int i = 0; i < R; ++i) store(i, 0);
+#pragma unroll
+  for (int i = 0; i < R; ++i) load(i, LT_K);  // zeros past K
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
-    const uint8_t* base = lds[s & 1] + l32 * LT_P + 16 * half;
+    const uint8_t* base = lds + (s & 1) * STAGE + l32 * LT_P + 16 * half;
 #pragma unroll
-    for (int k = 0; k < LT_K; k += 32) {
-      i32x4 a[2], b[2];
+    for (int k = 0; k < 4; ++k) {
+      i32x4 a[FB], b[FB];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        a[i] = *reinterpret_cast<const i32x4*>(base + (wn + 32 * i) * LT_P + k);
-        b[i] = *reinterpret_cast<const i32x4*>(base + (TN + wm + 32 * i) * LT_P + k);
+      for (int i = 0; i < FB; ++i) {
+        a[i] = *reinterpret_cast<const i32x4*>(base + (wn + 32 * i) * LT_P + 32 * k);
+        b[i] = *reinterpret_cast<const i32x4*>(base + (TL + wm + 32 * i) * LT_P + 32 * k);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < R / 4; ++i) {
+        store(k * (R / 4) + i, (s + 1) & 1);
+        load(k * (R / 4) + i, (s + 2) * LT_K);
+      }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
     }
-    if (s + 1 < steps) store((s + 1) & 1);
-    if (s + 2 < steps) load((s + 2) * LT_K);
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + wn + 32 * i + 8 * q + 4 * half;
+      float ws[4], bias[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        put4<T>(p, m0 + wm + 32 * j + l32, n0 + wn + 32 * i + 8 * q + 4 * half,
+      for (int e = 0; e < 4; ++e) {
+        const int c = min(n + e, p.N - 1);
+        ws[e] = p.ws[c];
+        bias[e] = p.bias != nullptr ? p.bias[c] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+        put4<T>(p, m0 + wm + 32 * j + l32, n, ws, bias,
                 (i32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}, wide);
+    }
+}
+
+template <typename T, int FB>
+pi_status launch_tile(pi_ctx* c, const LinDev& p, bool wide) {
+  const int tn = (p.N + 64 * FB - 1) / (64 * FB), tm = (p.M + 64 * FB - 1) / (64 * FB);
+  PI_HIP(c, allow_lds(k_q8_tile<T, FB>, tile_lds<FB>()));
+  PI_HIP(c, launch_kb(c, 0, k_q8_tile<T, FB>, dim3((unsigned)(tn * tm)), 256, tile_lds<FB>(), p, tn, tm, wide));
+  return PI_OK;
 }
 
 template <typename T>
 pi_status launch_linear(pi_ctx* c, const LinDev& p) {
   // 4 outputs in one store where every row starts at such a boundary
   const bool wide = p.y_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-  if (p.M > 256) {
-    PI_HIP(c, launch_k(c, 0, k_q8_tile<T>, dim3((p.N + 127) / 128, (p.M + 127) / 128), 0, p, wide));
-    return PI_OK;
+  // a tile's rows are addressed by 32-bit offsets
+  if (p.M > 256 && p.x_stride < (1 << 22) && p.w_stride < (1 << 22)) {
+    const long long big = (long long)((p.N + 255) / 256) * ((p.M + 255) / 256);
+    return big >= c->cus ? launch_tile<T, 4>(c, p, wide) : launch_tile<T, 2>(c, p, wide);
   }
   const int mb = std::min(4, (p.M + 15) / 16);
   const dim3 g((p.N + 31) / 32, (p.M + 16 * mb - 1) / (16 * mb));
