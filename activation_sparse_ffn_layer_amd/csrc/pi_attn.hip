@@ -124,6 +124,8 @@ __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o)
   return false;
 }
 
+__device__ u32x4 attn_zero;  // zeros, never written
+
 // LDS of a workgroup: keys, then values, of one tile (two where tiles are shared by waves). A
 // row's pitch is past the power of two: 16 bytes for K, whose rows are read 16 bytes a lane, 32
 // bytes for V, whose transposing reads take 32 bytes from each of 4 rows.
@@ -186,32 +188,40 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
   const bool piece_in = lc * 8 < a.D;
   uint8_t* const ks = smem + (OWN ? wk * KW * (KP + VP) : 0);
   const long long khead = (long long)hk * a.c.head_stride, nhead = (long long)hk * a.kv_head + (long long)b * a.kv_batch;
-  u32x4 kr[PASS], vr[PASS];
-  auto load = [&](int tile) {
+  // A tile's rows are loaded in two steps, their pages' numbers one tile ahead of the rows. What is
+  // not there is read from a zero in memory: a select after the load would wait for it.
+  constexpr int SETS = OWN ? 1 : 2;
+  u32x4 kr[SETS][PASS], vr[SETS][PASS];
+  int pg[PASS];
+  auto ids = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < PASS; ++i) {
       const int p = tile * KT + lr + i * RPP;
-      const uint8_t *kp = a.kn, *vp = a.vn;
-      bool ok = piece_in && p < total;
-      long long at = 0;
-      if (p < len) {
-        uint32_t off;
-        const int page = kv_page(a.c, b, page_of(a.c.div, (uint32_t)p, &off));
-        ok = ok && page >= 0;
-        at = (long long)page * a.c.page_stride + (long long)off * a.c.token_stride + khead;
-        kp = static_cast<const uint8_t*>(a.c.k);
-        vp = static_cast<const uint8_t*>(a.c.v);
-      } else {
-        at = (long long)(p - len) * a.kv_node + nhead;
-      }
-      at = ok ? at + lc * 8 : 0;
-      kr[i] = ld16_or0(kp + 2 * at, ok);
-      vr[i] = ld16_or0(vp + 2 * at, ok);
+      uint32_t off;
+      const uint32_t n = page_of(a.c.div, (uint32_t)min(p, max(len - 1, 0)), &off);
+      pg[i] = a.c.table == nullptr ? b : a.c.table[(long long)b * a.c.table_stride + n];
+    }
+  };
+  auto load = [&](int tile, int set) {
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int p = tile * KT + lr + i * RPP;
+      uint32_t off;
+      page_of(a.c.div, (uint32_t)p, &off);
+      const bool old = p < len;
+      const bool ok = piece_in && tile < ch.t1 && (old ? (unsigned)pg[i] < (unsigned)a.c.pages : p < total);
+      const long long at = lc * 8 + (old ? (long long)pg[i] * a.c.page_stride + (long long)off * a.c.token_stride + khead
+                                         : (long long)(p - len) * a.kv_node + nhead);
+      const uint8_t* kp = (old ? static_cast<const uint8_t*>(a.c.k) : a.kn) + 2 * at;
+      const uint8_t* vp = (old ? static_cast<const uint8_t*>(a.c.v) : a.vn) + 2 * at;
+      const uint8_t* zero = reinterpret_cast<const uint8_t*>(&attn_zero);
+      kr[set][i] = ld16(ok ? kp : zero);
+      vr[set][i] = ld16(ok ? vp : zero);
     }
   };
   // a stage is K rows, then V rows
   constexpr int STAGE = LROWS * (KP + VP);
-  auto store = [&](int tile, int stage) {
+  auto store = [&](int tile, int stage, int set) {
     uint8_t* base = ks + stage * STAGE;
     if (tile * KT + KT > len) {
       // A weight of zero times an infinity or a NaN is a NaN: such elements of the new nodes, whom
@@ -222,11 +232,11 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
         if (tile * KT + lr + i * RPP >= len) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t w = vr[i][e];
+            const uint32_t w = vr[set][i][e];
             const uint32_t lo = (w & Mm<T>::EXP) == Mm<T>::EXP ? 0xFFFFu : 0u;
             const uint32_t hi = (w & (Mm<T>::EXP << 16)) == Mm<T>::EXP << 16 ? 0xFFFF0000u : 0u;
             if (lo | hi) s_odd = 1;
-            vr[i][e] = w & ~(lo | hi);
+            vr[set][i][e] = w & ~(lo | hi);
           }
         }
     }
@@ -234,8 +244,8 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
     for (int i = 0; i < PASS; ++i) {
       const int r = lt / LPR + i * RPP;
       if (DP / 8 == LPR || lc < DP / 8) {
-        *reinterpret_cast<u32x4*>(base + r * KP + lc * 16) = kr[i];
-        *reinterpret_cast<u32x4*>(base + LROWS * KP + r * VP + lc * 16) = vr[i];
+        *reinterpret_cast<u32x4*>(base + r * KP + lc * 16) = kr[set][i];
+        *reinterpret_cast<u32x4*>(base + LROWS * KP + r * VP + lc * 16) = vr[set][i];
       }
     }
   };
@@ -317,27 +327,43 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
         }
   };
 
+  // the barriers for the compiler keep a tile's loads ahead of the products before it
+  ids(ch.t0);
+  load(ch.t0, 0);
   if constexpr (OWN) {
-    load(ch.t0);
+    ids(ch.t0 + 1);
     for (int t = ch.t0; t < ch.t1; ++t) {
-      store(t, 0);
+      store(t, 0, 0);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (t + 1 < ch.t1) load(t + 1);
+      load(t + 1, 0);
+      ids(t + 2);
+      __builtin_amdgcn_sched_barrier(0);
       compute(t, 0);
+      __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
   } else {
-    load(ch.t0);
-    store(ch.t0, 0);
-    if (ch.t0 + 1 < ch.t1) load(ch.t0 + 1);
+    ids(ch.t0 + 1);
+    load(ch.t0 + 1, 1);
+    ids(ch.t0 + 2);
+    store(ch.t0, 0, 0);
     __syncthreads();
-    for (int t = ch.t0; t < ch.t1; ++t) {
-      const int st = (t - ch.t0) & 1;
-      if (wave_live) compute(t, st);
-      if (t + 1 < ch.t1) store(t + 1, st ^ 1);
-      if (t + 2 < ch.t1) load(t + 2);
+    // tile t of stage h; registers h are free, the others hold tile t + 1
+    auto step = [&](int t, int h) {
+      load(t + 2, h);
+      ids(t + 3);
+      __builtin_amdgcn_sched_barrier(0);
+      if (wave_live) compute(t, h);
+      __builtin_amdgcn_sched_barrier(0);
+      store(t + 1, h ^ 1, h ^ 1);
       __syncthreads();
+    };
+    int t = ch.t0;
+    for (; t + 1 < ch.t1; t += 2) {
+      step(t, 0);
+      step(t + 1, 1);
     }
+    if (t < ch.t1) step(t, 0);
   }
 
   l = swap_add(l);
@@ -447,20 +473,44 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
   while (c > 1 && sum(c, a.B) > a.slots) c += max(1, c >> 5);
   const int first = sum(c, b), count = (tiles(b) + c - 1) / c;
   if (count == 1) return;
+  const long long at0 = ((long long)first * a.HK + hk) * a.R + r, next = (long long)a.HK * a.R;
   float m = -__builtin_inff();
-  for (int s = lane; s < count; s += WAVE) m = fmaxf(m, a.ml[2 * ((((long long)first + s) * a.HK + hk) * a.R + r)]);
+  for (int s = lane; s < count; s += WAVE) m = fmaxf(m, a.ml[2 * (at0 + s * next)]);
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, WAVE));
   const float base = m == -__builtin_inff() ? 0.f : m;
+  // Up to 128 columns the wave's halves take every other chunk.
+  constexpr int HALVES = DP <= 128 ? 2 : 1;
+  const int mine = HALVES == 2 ? lane >> 5 : 0, d = 4 * (HALVES == 2 ? lane & 31 : lane);
+  const float* part = a.part + at0 * DP + min(d, DP - 4);
   f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
-  const int d = 4 * lane;
-  for (int s = 0; s < count; ++s) {
-    const long long at = (((long long)first + s) * a.HK + hk) * a.R + r;
-    const float f = __builtin_amdgcn_exp2f(a.ml[2 * at] - base);
-    l += a.ml[2 * at + 1] * f;
-    if (d < a.D) v += *reinterpret_cast<const f32x4*>(a.part + at * DP + d) * f;
+  for (int s0 = 0; s0 < count; s0 += WAVE) {
+    // a lane's chunk of these 64: its factor and its part of the sum
+    const bool in = s0 + lane < count;
+    const long long at = at0 + (in ? s0 + lane : 0) * next;
+    const float f = in ? __builtin_amdgcn_exp2f(a.ml[2 * at] - base) : 0.f;
+    l += in ? a.ml[2 * at + 1] * f : 0.f;
+    const int n = min(WAVE, count - s0);
+    for (int s = 0; s < n; s += 8) {
+      constexpr int U = 8 / HALVES;
+      f32x4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const f32x4*>(part + (s0 + min(s + HALVES * u + mine, n - 1)) * next * DP);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = s + HALVES * u + mine;
+        v += x[u] * __shfl(c < n ? f : 0.f, min(c, n - 1), WAVE) * (c < n ? 1.f : 0.f);
+      }
+    }
   }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s, WAVE);
+  if constexpr (HALVES == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = swap_add(v[i]);
+  }
+  if (HALVES == 2 && lane >= 32) return;
   if (d >= a.D) return;
   T* o = reinterpret_cast<T*>(a.out) + (long long)b * a.out_batch + (long long)(r / a.G) * a.out_node +
          (long long)(hk * a.G + r % a.G) * a.out_head + d;

@@ -47,7 +47,8 @@ struct VfRow {    // a row; for a node also its own token's p and q under its pa
 };
 struct VfState {
   double c, left;
-  int32_t cur, next, depth, done;
+  int32_t cur, next, depth;
+  int32_t done;   // 1: the walk ended; 2, 3: with the weights of a pass of that parity
 };
 
 }  // namespace
@@ -98,10 +99,9 @@ __device__ __forceinline__ void logits8(const T* row, int i, int V, float (&o)[8
   }
 }
 
-// 2^t for t <= 0: 2^f of the fraction (|f| <= 1/2) by the polynomial of degree 9 through the
-// Chebyshev points of that interval, off by at most 3e-14; 0 below 2^-1000. A quarter of the
-// library's exp in instructions, which bounds the rows' pass.
-__device__ __forceinline__ double pow2(double t) {
+// 2^t for t <= 0, and 2^-1000 for all below that: 2^f of the fraction (|f| <= 1/2) by the polynomial
+// of degree 9 through the Chebyshev points of that interval, off by at most 3e-14.
+__device__ __forceinline__ double pow2_floor(double t) {
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: the sum's low bits are t's nearest whole number
   const double c = fmax(t, -1000.0);
   const double k = c + magic;
@@ -116,8 +116,11 @@ __device__ __forceinline__ double pow2(double t) {
   r = fma(r, f, 0.2402265069564034);
   r = fma(r, f, 0.6931471805599462);
   r = fma(r, f, 1.0);
-  const uint64_t b = __builtin_bit_cast(uint64_t, r) + (__builtin_bit_cast(uint64_t, k) << 52);
-  return t > -1000.0 ? __builtin_bit_cast(double, b) : 0.0;
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, r) + (__builtin_bit_cast(uint64_t, k) << 52));
+}
+__device__ __forceinline__ double pow2(double t) {
+  const double r = pow2_floor(t);
+  return t > -1000.0 ? r : 0.0;
 }
 // exp((z - m) / T), given it = log2(e) / T; z <= m, m finite
 __device__ __forceinline__ double expw(float z, float m, double it) { return pow2(((double)z - (double)m) * it); }
@@ -200,17 +203,20 @@ __device__ __forceinline__ void rest8(const VfDev& p, const VfShared& s, int b, 
   }
 }
 
-// A chunk's weight, by one wave; the same on every lane.
+// A chunk's weight, by one wave (part `k` of `of`); the same on every lane.
 template <typename T>
-__device__ __forceinline__ double rest_wave(const VfDev& p, const VfShared& s, int b, int kind, double it, int chunk) {
+__device__ __forceinline__ double rest_wave(const VfDev& p, const VfShared& s, int b, int kind, double it, int chunk, int k = 0,
+                                            int of = 1) {
   double v = 0.0, w[8];
-#pragma unroll 2
-  for (int g = 0; g < VF_CH / (8 * WAVE); ++g) {
+  const int each = VF_CH / (8 * WAVE) / of;
+#pragma unroll 4
+  for (int g = k * each; g < (k + 1) * each; ++g) {
     const int i = chunk * VF_CH + (g * WAVE + (int)threadIdx.x % WAVE) * 8;
-    if (i >= p.V) break;
-    rest8<T>(p, s, b, kind, it, i, w);
+    if (i < p.V) {
+      rest8<T>(p, s, b, kind, it, i, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v += w[j];
+      for (int j = 0; j < 8; ++j) v += w[j];
+    }
   }
   return wave_sum_d(v);
 }
@@ -413,9 +419,24 @@ __device__ __forceinline__ void to_the_end(const VfDev& p, VfShared& s, int b, d
   while (!s.st.done) {
     if (bins == nullptr) {
       double* own = rest_of(p, 1, b);
-      for (int k = threadIdx.x / WAVE; k < p.chunks; k += VF_NT / WAVE) {
-        const double v = rest_wave<T>(p, s, b, REST_Q, it, k);
-        if (threadIdx.x % WAVE == 0) own[k] = v;
+      constexpr int NW = VF_NT / WAVE;
+      const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+      const int of = p.chunks <= NW / 8 ? 8 : p.chunks <= NW / 4 ? 4 : p.chunks <= NW / 2 ? 2 : 1;  // waves per chunk
+      if (of == 1) {
+        for (int k = wave; k < p.chunks; k += NW) {
+          const double v = rest_wave<T>(p, s, b, REST_Q, it, k);
+          if (lane == 0) own[k] = v;
+        }
+      } else {
+        const double v = wave / of < p.chunks ? rest_wave<T>(p, s, b, REST_Q, it, wave / of, wave % of, of) : 0.0;
+        __syncthreads();
+        if (lane == 0) s.red[wave] = v;
+        __syncthreads();
+        if ((int)threadIdx.x < p.chunks) {
+          double t = 0.0;
+          for (int k = 0; k < of; ++k) t += s.red[threadIdx.x * of + k];
+          own[threadIdx.x] = t;
+        }
       }
       __threadfence_block();
       __syncthreads();
@@ -431,22 +452,26 @@ __device__ __forceinline__ void to_the_end(const VfDev& p, VfShared& s, int b, d
   finish<T, VF_NT>(p, s, b, it, bins);
 }
 
-// Bound by memory and by the exponentials, about 22 instructions of 64 bits per logit. A wave
-// takes its own 1024 logits' maximum as the base of its sum, so that the waves meet once.
-template <typename T>
+// Bound by memory and by the exponentials, about 20 instructions of 64 bits per logit. CW waves
+// share a chunk: with 4 each has 16 logits per lane and the waves' sums are joined in LDS; with 1
+// a lane has 64, which spreads the wave's sums and the loads' latency over more logits.
+template <typename T, int CW>
 __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   __shared__ VfPart w[NWAVES];
-  const int chunk = blockIdx.x, node = blockIdx.y, b = blockIdx.z;
+  const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+  const int chunk = CW == 1 ? (int)blockIdx.x * NWAVES + wave : (int)blockIdx.x, node = blockIdx.y, b = blockIdx.z;
+  if (CW == 1 && chunk >= p.chunks) return;
   const double it = inv_temp(p, b);
   const T* row = row_of<T>(p, b, node);
-  constexpr int G = VF_CH / (8 * BLOCK);
+  constexpr int G = VF_CH / (8 * WAVE * CW);
+  const int i0 = chunk * VF_CH + (CW == 1 ? lane : (int)threadIdx.x) * 8;
+  constexpr int STEP = 8 * WAVE * CW;
   float z[G][8];
   float m = -__builtin_inff();
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int i = chunk * VF_CH + g * (VF_CH / G) + (int)threadIdx.x * 8;
-    if (i < p.V) {
-      logits8(row, i, p.V, z[g]);
+    if (i0 + g * STEP < p.V) {
+      logits8(row, i0 + g * STEP, p.V, z[g]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[g][j] = -__builtin_inff();
@@ -462,37 +487,41 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   int at = 0x7FFFFFFF;
   if (m > -__builtin_inff()) {
     if (it != 0.0) {
+      // a weight below 2^-1000 of the largest counts as that: it does not change the sum
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += expw(z[g][j], m, it);
+        for (int j = 0; j < 8; ++j) sum += pow2_floor(((double)z[g][j] - (double)m) * it);
       sum = wave_sum_d(sum);
     } else {
 #pragma unroll
       for (int g = G - 1; g >= 0; --g)
 #pragma unroll
         for (int j = 7; j >= 0; --j)
-          if (z[g][j] == m) at = chunk * VF_CH + g * (VF_CH / G) + (int)threadIdx.x * 8 + j;
+          if (z[g][j] == m) at = i0 + g * STEP + j;
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1) at = min(at, __shfl_xor(at, o, WAVE));
     }
   }
-  if (threadIdx.x % WAVE == 0) w[threadIdx.x / WAVE] = VfPart{sum, m, at};
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  VfPart o = w[0];
+  VfPart o{sum, m, at};
+  if (CW > 1) {
+    if (lane == 0) w[wave] = o;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    o = w[0];
 #pragma unroll
-  for (int k = 1; k < NWAVES; ++k)
-    if (w[k].m > o.m || (w[k].m == o.m && w[k].at < o.at)) {
-      o.m = w[k].m;
-      o.at = w[k].at;
+    for (int k = 1; k < CW; ++k)
+      if (w[k].m > o.m || (w[k].m == o.m && w[k].at < o.at)) {
+        o.m = w[k].m;
+        o.at = w[k].at;
+      }
+    o.s = 0.0;
+    if (it != 0.0 && o.m > -__builtin_inff()) {
+#pragma unroll
+      for (int k = 0; k < CW; ++k) o.s += w[k].s * expw(w[k].m, o.m, it);
     }
-  o.s = 0.0;
-  if (it != 0.0 && o.m > -__builtin_inff()) {
-#pragma unroll
-    for (int k = 0; k < NWAVES; ++k) o.s += w[k].s * expw(w[k].m, o.m, it);
   }
-  p.part[((long long)b * p.N + node) * p.chunks + chunk] = o;
+  if (CW == 1 ? lane == 0 : true) p.part[((long long)b * p.N + node) * p.chunks + chunk] = o;
 }
 
 // The tree into LDS.
@@ -514,6 +543,16 @@ __global__ __launch_bounds__(VF_NT) void k_verify_walk(VfDev p, bool all) {
   const int b = blockIdx.x, lane = threadIdx.x % WAVE;
   const double it = inv_temp(p, b);
   load_nodes(p, s, b);
+  float zt = -__builtin_inff(), qv = 0.f;  // this node's token under its parent, loaded early
+  bool has = false;
+  if ((int)threadIdx.x < p.N) {
+    const int par = s.par[threadIdx.x], t = s.tok[threadIdx.x];
+    has = par >= 0 && (unsigned)t < (unsigned)p.V;
+    if (has) {
+      zt = clean(to_f32(row_of<T>(p, b, par)[t]));
+      if (p.q != nullptr) qv = p.q[(long long)b * p.qb + (long long)par * p.qn + t];
+    }
+  }
   // a wave per row joins its chunks, in a fixed order
   for (int i = threadIdx.x / WAVE; i < p.N; i += VF_NT / WAVE) {
     const VfPart* part = p.part + ((long long)b * p.N + i) * p.chunks;
@@ -549,13 +588,13 @@ __global__ __launch_bounds__(VF_NT) void k_verify_walk(VfDev p, bool all) {
   __syncthreads();
   const int i = threadIdx.x;
   if (i < p.N) {
-    const int par = s.par[i], t = s.tok[i];
-    double pt = 0.0, qt = 0.0;
-    if (par >= 0 && (unsigned)t < (unsigned)p.V) {
-      if (it == 0.0) pt = t == s.at[par] ? 1.0 : 0.0;
-      else if (s.rs[par] > 0.0) pt = expw(clean(to_f32(row_of<T>(p, b, par)[t])), s.m[par], it) * (1.0 / s.rs[par]);
-      if (p.q != nullptr) qt = (double)p.q[(long long)b * p.qb + (long long)par * p.qn + t];
+    const int par = s.par[i];
+    double pt = 0.0;
+    if (has) {
+      if (it == 0.0) pt = s.tok[i] == s.at[par] ? 1.0 : 0.0;
+      else if (s.rs[par] > 0.0) pt = expw(zt, s.m[par], it) * (1.0 / s.rs[par]);
     }
+    const double qt = (double)qv;
     s.pt[i] = pt;
     s.qt[i] = qt;
     if (!all) p.rows[(long long)b * p.N + i] = VfRow{s.rs[i], pt, qt, s.m[i], s.at[i]};
@@ -565,8 +604,8 @@ __global__ __launch_bounds__(VF_NT) void k_verify_walk(VfDev p, bool all) {
     p.nodes[(long long)b * p.N] = 0;
   }
   walk(p, s, b, it, true);
-  if (!all && threadIdx.x == 0) p.state[b] = s.st;
-  if (all || s.st.done) to_the_end<T>(p, s, b, it, nullptr);
+  if (all) to_the_end<T>(p, s, b, it, nullptr);
+  else if (threadIdx.x == 0) p.state[b] = s.st;
 }
 
 // What the walk left, into LDS; `pass`: how many passes were before.
@@ -593,7 +632,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rest(VfDev p, int pass) {
   const bool first = chunk == 0;
   VfState* now = p.state + (long long)((pass + 1) & 1) * p.B + b;
   if (p.state[(long long)(pass & 1) * p.B + b].done) {
-    if (first && threadIdx.x == 0) now->done = 1;
+    if (first && threadIdx.x == 0) *now = p.state[(long long)(pass & 1) * p.B + b];
     return;
   }
   load_state(p, s, b, pass);
@@ -606,9 +645,9 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rest(VfDev p, int pass) {
     if (threadIdx.x == 0) s.st.left = left;
     walk(p, s, b, it, first);
     if (s.st.done) {
-      if (first) {
-        finish<T, BLOCK>(p, s, b, it, bins);
-        if (threadIdx.x == 0) *now = s.st;
+      if (first && threadIdx.x == 0) {
+        *now = s.st;
+        now->done = 2 + ((pass - 1) & 1);
       }
       return;
     }
@@ -634,14 +673,17 @@ template <typename T>
 __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
   __shared__ VfShared s;
   const int b = blockIdx.x;
-  if (p.state[(long long)(passes & 1) * p.B + b].done) return;
   load_state(p, s, b, passes);
-  to_the_end<T>(p, s, b, inv_temp(p, b), rest_of(p, (passes - 1) & 1, b));
+  to_the_end<T>(p, s, b, inv_temp(p, b), rest_of(p, s.st.done > 1 ? s.st.done - 2 : (passes - 1) & 1, b));
 }
 
 template <typename T>
 pi_status launch_verify(pi_ctx* c, const VfDev& p) {
-  PI_HIP(c, launch_k(c, 0, k_verify_rows<T>, dim3(p.chunks, p.N, p.B), 0, p));
+  // a wave per chunk where that many waves fill the chip (8 per SIMD) all the same
+  if ((long long)p.chunks * p.N * p.B >= (long long)c->cus * 32)
+    PI_HIP(c, launch_k(c, 0, k_verify_rows<T, 1>, dim3((p.chunks + NWAVES - 1) / NWAVES, p.N, p.B), 0, p));
+  else
+    PI_HIP(c, launch_k(c, 0, k_verify_rows<T, NWAVES>, dim3(p.chunks, p.N, p.B), 0, p));
   const bool all = p.q == nullptr || p.N == 1 || p.chunks <= VF_OWN_CHUNKS;
   PI_HIP(c, launch_kb(c, 0, k_verify_walk<T>, dim3(p.B), VF_NT, 0, p, all));
   if (all) return PI_OK;

@@ -441,7 +441,7 @@ typedef struct pi_norm_args {
 pi_status pi_add_rmsnorm(pi_ctx *ctx, const pi_norm_args *args);
 
 /* A weight of N x K 8-bit integers with one scale per output channel.
- *   w          int8 [N][K], w_stride elements between rows (a multiple of 16); K a multiple of
+ *   w          int8 [N][K], w_stride elements between rows (a multiple of 16 below 2^22); K a multiple of
  *              16 below 131072 (the sums are exact in 32 bits)
  *   w_scale    fp32 [N]; bias fp32 [N] or NULL
  *   max_tokens limit of M, which sizes the scratch */
@@ -458,7 +458,7 @@ void pi_linear_destroy(pi_linear *lin);
 
 /* y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n] for M tokens, the sum in
  * whole numbers.
- *   x          int8 [M][K], x_stride a multiple of 16; x_scale fp32 [M]
+ *   x          int8 [M][K], x_stride a multiple of 16 below 2^22; x_scale fp32 [M]
  *   y          [M][N] of y_dtype; rows need no alignment beyond the element's */
 pi_status pi_linear_q8(pi_ctx *ctx, pi_linear *lin, const int8_t *x, int64_t x_stride, const float *x_scale, int32_t M,
                        void *y, int32_t y_dtype, int64_t y_stride);
