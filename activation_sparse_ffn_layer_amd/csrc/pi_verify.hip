@@ -1,24 +1,27 @@
 // Check of drafted tokens by rejection sampling (pi_verify).
 //
-// Which child of a node is taken depends on p(t) = exp((z_t - max) / T) / sum of its parent's row,
-// on the draft's q(t) and, after rejections, on c and the weight S that is left: after j of
-// them the residual is max(p - c q, 0) / S with c_{j+1} = c_j + S_j, S_{j+1} = sum_t max(p - c_{j+1} q, 0).
-// So no residual is ever stored: every pass recomputes it from the logits.
-//
-//   k_verify_rows   every row's maximum and sum, in chunks of the vocabulary
-//   k_verify_walk   a workgroup per sequence joins the chunks and walks the tree from its root, as
-//                   far as it can without a residual's weight
-//   k_verify_rest   the weight of one residual per sequence, in the same chunks. Every workgroup
-//                   first joins the chunks of the pass before and walks on, all alike, so that
-//                   no workgroup waits for another. Launched a fixed number of times (they
-//                   return at once where the sequence is done), then k_verify_end does
-//                   whatever is left. Vocabularies of few chunks have no such launch: the walk's
-//                   workgroup takes the residuals itself, a chunk per wave.
-// A walk that ends draws the next token: the chunk by the chunks' sums, then the token inside it.
+// Which child of a node is taken depends on p(t) = exp((z_t - max) / T) / Z of its parent's row (Z:
+// the row's sum), on the draft's q(t) and, after rejections, on c and the weight S that is left:
+// after j of them the residual is max(p - c q, 0) / S with c_{j+1} = c_j + S_j,
+// S_{j+1} = sum_t max(p - c_{j+1} q, 0). So no residual is ever stored: every pass recomputes it.
 //
 // The draws compare running sums over the vocabulary, whose steps are as small as 1e-6 of the
-// whole: exponentials and sums are in 64 bits throughout (a 32-bit exponential alone would move
-// one draw in some hundred).
+// whole, so a row that is drawn from, or whose residual is weighed, has its exponentials and
+// sums in 64 bits (a 32-bit exponential alone would move one draw in some hundred). Most rows of
+// a tree are only walked past: for them Z in 32 bits, off by less than 1e-5, decides, and a child
+// whose test is nearer than that waits for its row's Z in 64 bits.
+//
+//   k_verify_rows   every row's maximum and 32-bit sum, in chunks of the vocabulary: the one pass
+//                   over all logits, bound by memory
+//   k_verify_pass   walks the tree as far as it can, then sums in 64 bits, in the same chunks, what
+//                   the walk waits for: over the current row the exponentials (E), those of
+//                   the tokens with p > c q (A) and these tokens' q (Q). Then Z = E and
+//                   S = A / Z - c Q, exact to second order in the error of the 32-bit Z that
+//                   chose the tokens. Every workgroup walks for itself, all alike, so that
+//                   none waits for another. Launched a fixed number of times (they return at
+//                   once where the sequence is done).
+//   k_verify_end    a workgroup per sequence does whatever is left and draws the next token: the
+//                   chunk by the chunks' weights, then the token inside it.
 #include <algorithm>
 #include <new>
 
@@ -29,26 +32,29 @@ using namespace pi;
 
 namespace {
 
-constexpr int VF_CH = 4096;        // tokens per chunk: 16 per thread of a workgroup, 64 per lane of a wave
+constexpr int VF_CH = 4096;        // tokens per chunk
 constexpr int VF_MAX_NODES = 256;
-constexpr int VF_RESTS = 4;        // launches of k_verify_rest, where there are any
-constexpr int VF_NT = 1024;        // threads of the walk's workgroup
-constexpr int VF_OWN_CHUNKS = VF_NT / WAVE;  // up to so many chunks the walk's workgroup does all itself
+constexpr int VF_NT = 1024;        // threads of the workgroups that join all rows
+constexpr double VF_NEAR = 2e-5;   // a test with a 32-bit Z decides beyond this distance, relative to p
 
-struct VfPart {   // a chunk of a row
-  double s;       // sum of exp((z - m) / T)
-  float m;        // maximum
-  int32_t at;     // its lowest index (greedy rows only)
+struct VfPart {   // a chunk of a row, in 32 bits
+  float m, s;     // maximum, sum of exp((z - m) / T)
+  int32_t at;     // the maximum's lowest index (greedy rows only)
+  int32_t pad;
 };
-struct VfRow {    // a row; for a node also its own token's p and q under its parent
-  double s, pt, qt;
-  float m;
-  int32_t at;
+struct VfRow {    // a row; for a node also its own token's exp((z - m) / T) and q under its parent
+  double s, et;
+  float m, qt;
+  int32_t at, pad;
 };
+struct VfBin {    // a chunk of the current row, in 64 bits
+  double e, a, q;
+};
+enum { WAIT_REST = 0, WAIT_DRAW = 1, DONE = 2, DONE_PLAIN = 5 };
 struct VfState {
-  double c, left;
+  double c, left, z;  // z: the current row's sum in 64 bits, 0 before it is known
   int32_t cur, next, depth;
-  int32_t done;   // 1: the walk ended; 2, 3: with the weights of a pass of that parity
+  int32_t stage;      // WAIT_*: for a pass; DONE + i: ended, the weights to draw from in bins i
 };
 
 }  // namespace
@@ -60,7 +66,7 @@ struct pi_verifier {
   VfPart* part;     // [B][N][chunks]
   VfRow* rows;      // [B][N]
   VfState* state;   // [2][B], by the parity of the pass
-  double* rest;     // [3][B][chunks]: two passes' weights; the walk's own
+  VfBin* bins;      // [3][B][chunks]: two passes' by parity; the last kernel's own
 };
 
 namespace {
@@ -76,7 +82,7 @@ struct VfDev {
   VfPart* part;
   VfRow* rows;
   VfState* state;
-  double* rest;
+  VfBin* bins;
 };
 
 // NaN to -inf, +inf to the largest finite value
@@ -131,16 +137,16 @@ __device__ __forceinline__ double wave_sum_d(double v) {
   return v;
 }
 
-// Sum over the workgroup's NT threads, the same on every thread; red: NT / WAVE doubles.
+// Sums over the workgroup's NT threads, the same on every thread; red: 3 NT / WAVE doubles.
 template <int NT>
-__device__ __forceinline__ double block_sum_d(double v, double* red) {
-  v = wave_sum_d(v);
+__device__ __forceinline__ VfBin block_sum(VfBin v, VfBin* red) {
+  v = VfBin{wave_sum_d(v.e), wave_sum_d(v.a), wave_sum_d(v.q)};
   __syncthreads();
   if (threadIdx.x % WAVE == 0) red[threadIdx.x / WAVE] = v;
   __syncthreads();
-  double s = 0.0;
+  VfBin s{0.0, 0.0, 0.0};
 #pragma unroll
-  for (int i = 0; i < NT / WAVE; ++i) s += red[i];
+  for (int i = 0; i < NT / WAVE; ++i) s = VfBin{s.e + red[i].e, s.a + red[i].a, s.q + red[i].q};
   return s;
 }
 
@@ -152,29 +158,29 @@ __device__ __forceinline__ double inv_temp(const VfDev& p, int b) {  // log2(e) 
   const float t = p.temp == nullptr ? 1.f : p.temp[b];
   return t > 0.f ? 1.4426950408889634 / (double)t : 0.0;
 }
-// Weights of a pass (0, 1, by its parity) or of the walk itself (2).
-__device__ __forceinline__ double* rest_of(const VfDev& p, int which, int b) {
-  return p.rest + ((long long)which * p.B + b) * p.chunks;
+__device__ __forceinline__ VfBin* bins_of(const VfDev& p, int which, int b) {
+  return p.bins + ((long long)which * p.B + b) * p.chunks;
 }
 
 struct VfShared {
-  double pt[VF_MAX_NODES], qt[VF_MAX_NODES], rs[VF_MAX_NODES];
-  float m[VF_MAX_NODES], u[VF_MAX_NODES];
+  double et[VF_MAX_NODES], rs[VF_MAX_NODES];
+  float m[VF_MAX_NODES], u[VF_MAX_NODES], qt[VF_MAX_NODES];
   int32_t at[VF_MAX_NODES], par[VF_MAX_NODES], tok[VF_MAX_NODES];
   VfState st;
-  double red[VF_NT / WAVE];
+  VfBin red[VF_NT / WAVE];
   double target, before;
   int32_t pick, last;
 };
 
-// The weights that are left, from token i on: p, p - c q or p without the children's tokens.
-enum { REST_P = 0, REST_Q = 1, REST_KIDS = 2 };
+// 8 tokens of the current row from i on: exp((z - m) / T), the draft's q (0 without one), and a bit
+// for each token that the draw may give: without a q, not the children's.
 template <typename T>
-__device__ __forceinline__ void rest8(const VfDev& p, const VfShared& s, int b, int kind, double it, int i, double (&w)[8]) {
+__device__ __forceinline__ uint32_t row8(const VfDev& p, const VfShared& s, int b, double it, int i, double (&e)[8],
+                                         float (&q)[8]) {
   const int cur = s.st.cur;
-  float z[8], q[8];
+  float z[8];
   logits8(row_of<T>(p, b, cur), i, p.V, z);
-  if (kind == REST_Q) {
+  if (p.q != nullptr) {
     const float* qr = p.q + (long long)b * p.qb + (long long)cur * p.qn;
     if (i + 8 <= p.V) {
       __builtin_memcpy(q, qr + i, sizeof q);
@@ -182,97 +188,90 @@ __device__ __forceinline__ void rest8(const VfDev& p, const VfShared& s, int b, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) q[j] = i + j < p.V ? qr[i + j] : 0.f;
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = 0.f;
   }
   const float m = s.m[cur];
-  const double is = 1.0 / s.rs[cur];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = expw(z[j], m, it) * is;
-  if (kind == REST_Q) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < p.V) w[j] = fmax(w[j] - s.st.c * (double)q[j], 0.0);
-  } else if (kind == REST_KIDS) {
+  for (int j = 0; j < 8; ++j) e[j] = expw(z[j], m, it);
+  uint32_t may = 0xFF;
+  if (p.q == nullptr)
     for (int k = cur + 1; k < p.N; ++k) {
       const int t = s.tok[k] - i;
-      if (s.par[k] == cur && t >= 0 && t < 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (t == j) w[j] = 0.0;
-      }
+      if (s.par[k] == cur && t >= 0 && t < 8) may &= ~(1u << t);
     }
-  }
+  return may;
 }
 
-// A chunk's weight, by one wave (part `k` of `of`); the same on every lane.
+// 8 tokens' part of a chunk's sums.
 template <typename T>
-__device__ __forceinline__ double rest_wave(const VfDev& p, const VfShared& s, int b, int kind, double it, int chunk, int k = 0,
-                                            int of = 1) {
-  double v = 0.0, w[8];
-  const int each = VF_CH / (8 * WAVE) / of;
-#pragma unroll 4
-  for (int g = k * each; g < (k + 1) * each; ++g) {
-    const int i = chunk * VF_CH + (g * WAVE + (int)threadIdx.x % WAVE) * 8;
-    if (i < p.V) {
-      rest8<T>(p, s, b, kind, it, i, w);
+__device__ __forceinline__ void bin8(const VfDev& p, const VfShared& s, int b, double it, int i, VfBin* v) {
+  if (i >= p.V) return;
+  double e[8];
+  float q[8];
+  const uint32_t may = row8<T>(p, s, b, it, i, e, q);
+  const double iz = 1.0 / (s.st.z > 0.0 ? s.st.z : s.rs[s.st.cur]), c = s.st.c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v += w[j];
-    }
+  for (int j = 0; j < 8; ++j) {
+    const bool in = ((may >> j) & 1) && e[j] * iz > c * (double)q[j];
+    v->e += e[j];
+    v->a += in ? e[j] : 0.0;
+    v->q += in ? (double)q[j] : 0.0;
   }
-  return wave_sum_d(v);
 }
 
-// Draw the next token at node s.st.cur and write the sequence's outputs. All NT threads; `bins`:
-// the chunks' weights of the residual that is left, where the walk ended on one.
+// A chunk's sums by the workgroup's NT threads, the same on every thread.
 template <typename T, int NT>
-__device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, double it, const double* bins) {
+__device__ __forceinline__ VfBin bin_block(const VfDev& p, VfShared& s, int b, double it, int chunk) {
+  VfBin v{0.0, 0.0, 0.0};
+#pragma unroll
+  for (int g = 0; g < VF_CH / 8; g += NT)
+    if (NT <= VF_CH / 8 || threadIdx.x < VF_CH / 8) bin8<T>(p, s, b, it, chunk * VF_CH + (g + (int)threadIdx.x) * 8, &v);
+  return block_sum<NT>(v, s.red);
+}
+
+// The sums of the pass that the walk waited for: Z and the residual's weight.
+template <int NT>
+__device__ __forceinline__ void join_bins(const VfDev& p, VfShared& s, const VfBin* bins) {
+  VfBin v{0.0, 0.0, 0.0};
+  for (int k = threadIdx.x; k < p.chunks; k += NT) v = VfBin{v.e + bins[k].e, v.a + bins[k].a, v.q + bins[k].q};
+  v = block_sum<NT>(v, s.red);
+  if (threadIdx.x == 0) {
+    s.st.z = v.e;
+    s.st.left = s.st.c > 0.0 ? fmax(v.a / v.e - s.st.c * v.q, 0.0) : 1.0;
+  }
+  __syncthreads();
+}
+
+// Draw the next token at node s.st.cur and write the sequence's outputs. All VF_NT threads.
+template <typename T>
+__device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, double it) {
+  constexpr int NT = VF_NT;
   const int cur = s.st.cur, lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
   int next = -1;
-  if (it == 0.0) {
-    next = s.at[cur];
-  } else if (s.rs[cur] > 0.0) {
-    double* own = rest_of(p, 2, b);
-    int kind = p.q != nullptr ? (s.st.c > 0.0 ? REST_Q : REST_P) : REST_KIDS;
-    const VfPart* part = p.part + ((long long)b * p.N + cur) * p.chunks;
-    auto own_bins = [&]() {  // p itself, from the rows' pass
-      for (int k = threadIdx.x; k < p.chunks; k += NT)
-        own[k] = part[k].s > 0.0 ? part[k].s * expw(part[k].m, s.m[cur], it) / s.rs[cur] : 0.0;
-      __threadfence_block();
-      __syncthreads();
-      bins = own;
-    };
-    if (kind != REST_Q) own_bins();
-    if (kind == REST_KIDS) {  // the chunks that lose a token are summed again, a wave per child
-      int nth = 0;
-      for (int k = cur + 1; k < p.N; ++k) {
-        if (s.par[k] != cur || (unsigned)s.tok[k] >= (unsigned)p.V || nth++ % (NT / WAVE) != wave) continue;
-        const int ch = s.tok[k] / VF_CH;
-        const double v = rest_wave<T>(p, s, b, kind, it, ch);
-        if (lane == 0) own[ch] = v;  // children of one chunk write the same
-      }
-      __threadfence_block();
-      __syncthreads();
+  if (s.st.stage == DONE_PLAIN) {
+    if (it == 0.0) next = s.at[cur];
+  } else {
+    const VfBin* bins = bins_of(p, s.st.stage - DONE, b);
+    VfBin sum{0.0, 0.0, 0.0};
+    for (int k = threadIdx.x; k < p.chunks; k += NT) sum = VfBin{sum.e + bins[k].e, sum.a + bins[k].a, sum.q + bins[k].q};
+    sum = block_sum<NT>(sum, s.red);
+    // the chunks' weights: of what is left, or of p where nothing is
+    const double iz = 1.0 / sum.e, c = p.q != nullptr ? s.st.c : 0.0;
+    const bool left = sum.a * iz - c * sum.q > 0.0;
+    auto weight = [&](int k) { return left ? fmax(bins[k].a * iz - c * bins[k].q, 0.0) : bins[k].e * iz; };
+    double total = 0.0;
+    for (int k = threadIdx.x; k < p.chunks; k += NT) total += weight(k);
+    total = block_sum<NT>(VfBin{total, 0.0, 0.0}, s.red).e;
+    if (threadIdx.x == 0) {
+      s.before = 0.0;
+      s.pick = 0x7FFFFFFF;
+      s.last = -1;
     }
-    for (int attempt = 0; attempt < 2; ++attempt) {
-      double total = 0.0;
-      for (int k = threadIdx.x; k < p.chunks; k += NT) total += bins[k];
-      total = block_sum_d<NT>(total, s.red);
-      if (threadIdx.x == 0) {
-        s.target = (double)p.u_next[b] * total;
-        s.before = 0.0;
-        s.pick = 0x7FFFFFFF;
-        s.last = -1;
-      }
-      __syncthreads();
-      if (total > 0.0 || attempt == 1) break;
-      kind = REST_P;
-      own_bins();
-    }
-    // the chunk whose running sum passes the target, or the last one with any weight
-    const double target = s.target;
-    double carry = 0.0;
-    for (int k0 = 0; k0 < p.chunks; k0 += NT) {
-      const int k = k0 + (int)threadIdx.x;
-      const double v = k < p.chunks ? bins[k] : 0.0;
+    __syncthreads();
+    // inclusive sum over the workgroup of one value per thread, from `carry` on
+    auto scan = [&](double v, double* carry) {
       double incl = v;
 #pragma unroll
       for (int o = 1; o < WAVE; o <<= 1) {
@@ -280,14 +279,22 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
         if (lane >= o) incl += t;
       }
       __syncthreads();
-      if (lane == WAVE - 1) s.red[wave] = incl;
+      if (lane == WAVE - 1) s.red[wave].e = incl;
       __syncthreads();
-      double run = carry;
+      double run = *carry;
       for (int i = 0; i < NT / WAVE; ++i) {
-        if (i < wave) run += s.red[i];
-        carry += s.red[i];
+        if (i < wave) run += s.red[i].e;
+        *carry += s.red[i].e;
       }
-      run += incl;
+      return run + incl;
+    };
+    // the chunk whose running sum passes the target, or the last one with any weight
+    const double target = (double)p.u_next[b] * total;
+    double carry = 0.0;
+    for (int k0 = 0; k0 < p.chunks; k0 += NT) {
+      const int k = k0 + (int)threadIdx.x;
+      const double v = k < p.chunks ? weight(k) : 0.0;
+      const double run = scan(v, &carry);
       if (v > 0.0 && run > target) atomicMin(&s.pick, k);
       if (v > 0.0) atomicMax(&s.last, k);
       __syncthreads();
@@ -303,38 +310,31 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
       s.pick = 0x7FFFFFFF;
       s.last = -1;
     }
-    if (chunk >= 0) {  // the token: TPT tokens per thread in order, threads in order
-      constexpr int TPT = VF_CH / NT < 8 ? 8 : VF_CH / NT;
-      double w[TPT], sum = 0.0;
+    if (chunk >= 0) {  // the token: 8 per thread in order, threads in order
+      double w[8], all = 0.0;
       int lastw = -1;
-      const int i0 = chunk * VF_CH + (int)threadIdx.x * TPT;
+      const int i = chunk * VF_CH + (int)threadIdx.x * 8;
+      const bool in = threadIdx.x < VF_CH / 8 && i < p.V;
+      if (in) {
+        double e[8];
+        float q[8];
+        const uint32_t may = row8<T>(p, s, b, it, i, e, q);
 #pragma unroll
-      for (int g = 0; g < TPT; g += 8) {
-        double w8[8];
-        const bool in = threadIdx.x * TPT < VF_CH && i0 + g < p.V;
-        if (in) rest8<T>(p, s, b, kind, it, i0 + g, w8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          w[g + j] = in ? w8[j] : 0.0;
-          sum += w[g + j];
-          if (w[g + j] > 0.0) lastw = i0 + g + j;
-        }
+        for (int j = 0; j < 8; ++j) w[j] = !left ? e[j] * iz : (may >> j) & 1 ? fmax(e[j] * iz - c * (double)q[j], 0.0) : 0.0;
       }
-      double incl = sum;
 #pragma unroll
-      for (int o = 1; o < WAVE; o <<= 1) {
-        const double t = __shfl_up(incl, o, WAVE);
-        if (lane >= o) incl += t;
+      for (int j = 0; j < 8; ++j) {
+        if (!in) w[j] = 0.0;
+        all += w[j];
+        if (w[j] > 0.0) lastw = i + j;
       }
-      if (lane == WAVE - 1) s.red[wave] = incl;
-      __syncthreads();
-      double run = incl - sum;
-      for (int i = 0; i < wave; ++i) run += s.red[i];
+      carry = 0.0;
+      double run = scan(all, &carry) - all;
       int mine = 0x7FFFFFFF;
 #pragma unroll
-      for (int j = 0; j < TPT; ++j) {
+      for (int j = 0; j < 8; ++j) {
         run += w[j];
-        if (w[j] > 0.0 && run > rest) mine = min(mine, i0 + j);
+        if (w[j] > 0.0 && run > rest) mine = min(mine, i + j);
       }
       if (mine != 0x7FFFFFFF) atomicMin(&s.pick, mine);
       if (lastw >= 0) atomicMax(&s.last, lastw);
@@ -353,15 +353,15 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
   if (threadIdx.x == 0) p.n[b] = depth;
 }
 
-// Walk on from s.st until a residual's weight is needed or no child is left to try (s.st.done).
-// All threads; the first wave walks, all its lanes on the same values. `write`: the path goes to
-// memory.
-__device__ __forceinline__ void walk(const VfDev& p, VfShared& s, int b, double it, bool write) {
+// Walk on from s.st until a pass is needed or no child is left to try. All threads; the first wave
+// walks, all its lanes on the same values. `src`: the bins of the pass just joined, if any;
+// `write`: the path goes to memory.
+__device__ __forceinline__ void walk(const VfDev& p, VfShared& s, int b, double it, int src, bool write) {
   __syncthreads();
   if (threadIdx.x < WAVE) {
     const int lane = threadIdx.x;
     int cur = s.st.cur, next = s.st.next, depth = s.st.depth;
-    double c = s.st.c, left = s.st.left;
+    double c = s.st.c, left = s.st.left, z = s.st.z;
     bool end = true;
     for (int g = next / WAVE; g * WAVE < p.N;) {
       const int i0 = g * WAVE + lane;
@@ -371,97 +371,68 @@ __device__ __forceinline__ void walk(const VfDev& p, VfShared& s, int b, double 
         continue;
       }
       const int i = g * WAVE + __ffsll((unsigned long long)kids) - 1;
-      next = i + 1;
-      const double pt = s.pt[i], u = (double)s.u[i];
-      bool take;
-      if (p.q != nullptr) {
-        const double qt = s.qt[i];
-        take = u * left * qt < fmax(pt - c * qt, 0.0);
-        if (!take) {
-          c += left;
-          if (it == 0.0) {  // all weight at one token
-            const int a = s.at[cur];
-            left = a >= 0 ? fmax(1.0 - c * (double)p.q[(long long)b * p.qb + (long long)cur * p.qn + a], 0.0) : 0.0;
-          } else if (left > 0.0) {
-            end = false;
-          }
-        }
-      } else {
-        bool again = false;
+      const double sum = z > 0.0 ? z : s.rs[cur], u = (double)s.u[i], qt = (double)s.qt[i];
+      const double pt = it == 0.0 ? (s.tok[i] == s.at[cur] ? 1.0 : 0.0) : sum > 0.0 ? s.et[i] / sum : 0.0;
+      bool again = false;  // without a q: an earlier child's token
+      if (p.q == nullptr)
         for (int k0 = 0; k0 < i; k0 += WAVE) {
           const int k = k0 + lane;
           again = again || __any(k < i && s.par[k] == cur && s.tok[k] == s.tok[i]);
         }
-        take = !again && u * left < pt;
-        if (!take && !again) left -= pt;
+      const double lhs = p.q != nullptr ? u * left * qt : u * left, rhs = p.q != nullptr ? fmax(pt - c * qt, 0.0) : pt;
+      if (it != 0.0 && z == 0.0 && pt > 0.0 && !again && fabs(lhs - rhs) <= VF_NEAR * (pt + (p.q != nullptr ? 0.0 : u))) {
+        next = cur + 1;  // the row again, with its sum in 64 bits
+        c = 0.0;
+        left = 1.0;
+        end = false;
+        break;
       }
+      next = i + 1;
+      const bool take = !again && lhs < rhs;
       if (take) {
         cur = i;
         c = 0.0;
         left = 1.0;
+        z = 0.0;
         if (write && lane == 0) p.nodes[(long long)b * p.N + depth] = i;
         ++depth;
+      } else if (p.q != nullptr) {
+        c += left;
+        if (it == 0.0) {  // all weight at one token
+          const int a = s.at[cur];
+          left = a >= 0 ? fmax(1.0 - c * (double)p.q[(long long)b * p.qb + (long long)cur * p.qn + a], 0.0) : 0.0;
+        } else if (left > 0.0 && sum > 0.0) {
+          end = false;
+          break;
+        }
+      } else if (!again) {
+        left -= pt;
       }
-      if (!end) break;
       g = next / WAVE;
     }
-    if (lane == 0) s.st = VfState{c, left, cur, next, depth, end ? 1 : 0};
+    int stage = WAIT_REST;
+    if (end) {
+      if (it == 0.0 || s.rs[cur] == 0.0) stage = DONE_PLAIN;
+      else if (p.q != nullptr && c > 0.0) stage = DONE + src;
+      else stage = WAIT_DRAW;
+    }
+    if (lane == 0) s.st = VfState{c, left, z, cur, next, depth, stage};
   }
   __threadfence_block();
   __syncthreads();
 }
 
-// What is left to do for a sequence, by its own workgroup: walk on, with the residuals of `bins`
-// where the state waits for one.
-template <typename T>
-__device__ __forceinline__ void to_the_end(const VfDev& p, VfShared& s, int b, double it, const double* bins) {
-  // at most one round per node: each consumes a child
-  while (!s.st.done) {
-    if (bins == nullptr) {
-      double* own = rest_of(p, 1, b);
-      constexpr int NW = VF_NT / WAVE;
-      const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
-      const int of = p.chunks <= NW / 8 ? 8 : p.chunks <= NW / 4 ? 4 : p.chunks <= NW / 2 ? 2 : 1;  // waves per chunk
-      if (of == 1) {
-        for (int k = wave; k < p.chunks; k += NW) {
-          const double v = rest_wave<T>(p, s, b, REST_Q, it, k);
-          if (lane == 0) own[k] = v;
-        }
-      } else {
-        const double v = wave / of < p.chunks ? rest_wave<T>(p, s, b, REST_Q, it, wave / of, wave % of, of) : 0.0;
-        __syncthreads();
-        if (lane == 0) s.red[wave] = v;
-        __syncthreads();
-        if ((int)threadIdx.x < p.chunks) {
-          double t = 0.0;
-          for (int k = 0; k < of; ++k) t += s.red[threadIdx.x * of + k];
-          own[threadIdx.x] = t;
-        }
-      }
-      __threadfence_block();
-      __syncthreads();
-      bins = own;
-    }
-    double left = 0.0;
-    for (int k = threadIdx.x; k < p.chunks; k += VF_NT) left += bins[k];
-    left = block_sum_d<VF_NT>(left, s.red);
-    if (threadIdx.x == 0) s.st.left = left;
-    walk(p, s, b, it, true);
-    if (!s.st.done) bins = nullptr;
-  }
-  finish<T, VF_NT>(p, s, b, it, bins);
-}
-
-// Bound by memory and by the exponentials, about 20 instructions of 64 bits per logit. CW waves
-// share a chunk: with 4 each has 16 logits per lane and the waves' sums are joined in LDS; with 1
-// a lane has 64, which spreads the wave's sums and the loads' latency over more logits.
+// Bound by memory. CW waves share a chunk: with 4 each has 16 logits per lane and the waves' sums
+// are joined in LDS; with 1 a lane has 64, which spreads the wave's sums and the loads' latency
+// over more logits.
 template <typename T, int CW>
 __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   __shared__ VfPart w[NWAVES];
   const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
   const int chunk = CW == 1 ? (int)blockIdx.x * NWAVES + wave : (int)blockIdx.x, node = blockIdx.y, b = blockIdx.z;
   if (CW == 1 && chunk >= p.chunks) return;
-  const double it = inv_temp(p, b);
+  const double itd = inv_temp(p, b);
+  const float it = fminf((float)itd, 3e38f);
   const T* row = row_of<T>(p, b, node);
   constexpr int G = VF_CH / (8 * WAVE * CW);
   const int i0 = chunk * VF_CH + (CW == 1 ? lane : (int)threadIdx.x) * 8;
@@ -483,16 +454,18 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
     for (int j = 0; j < 8; ++j) m = fmaxf(m, z[g][j]);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
-  double sum = 0.0;
+  float sum = 0.f;
   int at = 0x7FFFFFFF;
   if (m > -__builtin_inff()) {
-    if (it != 0.0) {
-      // a weight below 2^-1000 of the largest counts as that: it does not change the sum
+    if (itd != 0.0) {
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += pow2_floor(((double)z[g][j] - (double)m) * it);
-      sum = wave_sum_d(sum);
+        for (int j = 0; j < 8; ++j) part[j & 3] += __builtin_amdgcn_exp2f((z[g][j] - m) * it);
+      sum = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, WAVE);
     } else {
 #pragma unroll
       for (int g = G - 1; g >= 0; --g)
@@ -503,7 +476,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
       for (int o = 32; o > 0; o >>= 1) at = min(at, __shfl_xor(at, o, WAVE));
     }
   }
-  VfPart o{sum, m, at};
+  VfPart o{m, sum, at, 0};
   if (CW > 1) {
     if (lane == 0) w[wave] = o;
     __syncthreads();
@@ -515,11 +488,10 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
         o.m = w[k].m;
         o.at = w[k].at;
       }
-    o.s = 0.0;
-    if (it != 0.0 && o.m > -__builtin_inff()) {
+    o.s = 0.f;
 #pragma unroll
-      for (int k = 0; k < CW; ++k) o.s += w[k].s * expw(w[k].m, o.m, it);
-    }
+    for (int k = 0; k < CW; ++k)
+      if (w[k].s > 0.f) o.s += w[k].s * __builtin_amdgcn_exp2f((w[k].m - o.m) * it);
   }
   if (CW == 1 ? lane == 0 : true) p.part[((long long)b * p.N + node) * p.chunks + chunk] = o;
 }
@@ -536,86 +508,70 @@ __device__ __forceinline__ void load_nodes(const VfDev& p, VfShared& s, int b) {
   }
 }
 
-// With `all` the sequence is brought to its end here.
+// The first pass's start: all rows' sums in LDS (and, from one workgroup, in memory).
 template <typename T>
-__global__ __launch_bounds__(VF_NT) void k_verify_walk(VfDev p, bool all) {
-  __shared__ VfShared s;
-  const int b = blockIdx.x, lane = threadIdx.x % WAVE;
-  const double it = inv_temp(p, b);
+__device__ __forceinline__ void join_rows(const VfDev& p, VfShared& s, int b, double it, bool write) {
+  const int lane = threadIdx.x % WAVE;
   load_nodes(p, s, b);
-  float zt = -__builtin_inff(), qv = 0.f;  // this node's token under its parent, loaded early
+  __syncthreads();
+  float zt = 0.f, qt = 0.f;  // this node's token under its parent, loaded early
   bool has = false;
-  if ((int)threadIdx.x < p.N) {
-    const int par = s.par[threadIdx.x], t = s.tok[threadIdx.x];
+  const int i = threadIdx.x;
+  if (i < p.N) {
+    const int par = s.par[i], t = s.tok[i];
     has = par >= 0 && (unsigned)t < (unsigned)p.V;
     if (has) {
-      zt = clean(to_f32(row_of<T>(p, b, par)[t]));
-      if (p.q != nullptr) qv = p.q[(long long)b * p.qb + (long long)par * p.qn + t];
+      zt = to_f32(row_of<T>(p, b, par)[t]);
+      if (p.q != nullptr) qt = p.q[(long long)b * p.qb + (long long)par * p.qn + t];
     }
   }
   // a wave per row joins its chunks, in a fixed order
-  for (int i = threadIdx.x / WAVE; i < p.N; i += VF_NT / WAVE) {
-    const VfPart* part = p.part + ((long long)b * p.N + i) * p.chunks;
+  for (int r = threadIdx.x / WAVE; r < p.N; r += VF_NT / WAVE) {
+    const VfPart* part = p.part + ((long long)b * p.N + r) * p.chunks;
     float m = -__builtin_inff();
-    double sum = 0.0;
-    int at = 0x7FFFFFFF;
-    if (p.chunks <= WAVE) {
-      const VfPart o = lane < p.chunks ? part[lane] : VfPart{0.0, -__builtin_inff(), 0x7FFFFFFF};
-      m = o.m;
+    VfPart o{m, 0.f, 0x7FFFFFFF, 0};
+    if (lane < p.chunks) o = part[lane];
+    m = o.m;
+    for (int k = lane + WAVE; k < p.chunks; k += WAVE) m = fmaxf(m, part[k].m);
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
-      if (o.m == m) at = o.at;
-      if (o.s > 0.0) sum = o.s * expw(o.m, m, it);
-    } else {
-      for (int k = lane; k < p.chunks; k += WAVE) m = fmaxf(m, part[k].m);
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
-      for (int k = lane; k < p.chunks; k += WAVE) {
-        const VfPart o = part[k];
-        if (o.m == m) at = min(at, o.at);
-        if (o.s > 0.0) sum += o.s * expw(o.m, m, it);
-      }
+    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
+    int at = o.m == m ? o.at : 0x7FFFFFFF;
+    double sum = o.s > 0.f ? (double)o.s * expw(o.m, m, it) : 0.0;
+    for (int k = lane + WAVE; k < p.chunks; k += WAVE) {
+      const VfPart n = part[k];
+      if (n.m == m) at = min(at, n.at);
+      if (n.s > 0.f) sum += (double)n.s * expw(n.m, m, it);
     }
     sum = wave_sum_d(sum);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) at = min(at, __shfl_xor(at, d, WAVE));
     if (lane == 0) {
-      s.m[i] = m;
-      s.at[i] = at == 0x7FFFFFFF ? -1 : at;
-      s.rs[i] = sum;
+      s.m[r] = m;
+      s.at[r] = at == 0x7FFFFFFF ? -1 : at;
+      s.rs[r] = sum;
     }
   }
   __syncthreads();
-  const int i = threadIdx.x;
   if (i < p.N) {
-    const int par = s.par[i];
-    double pt = 0.0;
-    if (has) {
-      if (it == 0.0) pt = s.tok[i] == s.at[par] ? 1.0 : 0.0;
-      else if (s.rs[par] > 0.0) pt = expw(zt, s.m[par], it) * (1.0 / s.rs[par]);
-    }
-    const double qt = (double)qv;
-    s.pt[i] = pt;
+    const double et = has && s.m[s.par[i]] > -__builtin_inff() ? expw(clean(zt), s.m[s.par[i]], it) : 0.0;
+    s.et[i] = et;
     s.qt[i] = qt;
-    if (!all) p.rows[(long long)b * p.N + i] = VfRow{s.rs[i], pt, qt, s.m[i], s.at[i]};
+    if (write) p.rows[(long long)b * p.N + i] = VfRow{s.rs[i], et, s.m[i], qt, s.at[i], 0};
   }
-  if (threadIdx.x == 0) {
-    s.st = VfState{0.0, 1.0, 0, 1, 1, 0};
-    p.nodes[(long long)b * p.N] = 0;
+  if (i == 0) {
+    s.st = VfState{0.0, 1.0, 0.0, 0, 1, 1, WAIT_REST};
+    if (write) p.nodes[(long long)b * p.N] = 0;
   }
-  walk(p, s, b, it, true);
-  if (all) to_the_end<T>(p, s, b, it, nullptr);
-  else if (threadIdx.x == 0) p.state[b] = s.st;
 }
 
-// What the walk left, into LDS; `pass`: how many passes were before.
+// What the passes before `pass` left, into LDS.
 __device__ __forceinline__ void load_state(const VfDev& p, VfShared& s, int b, int pass) {
   load_nodes(p, s, b);
   const int i = threadIdx.x;
   if (i < p.N) {
     const VfRow r = p.rows[(long long)b * p.N + i];
     s.rs[i] = r.s;
-    s.pt[i] = r.pt;
+    s.et[i] = r.et;
     s.qt[i] = r.qt;
     s.m[i] = r.m;
     s.at[i] = r.at;
@@ -624,57 +580,65 @@ __device__ __forceinline__ void load_state(const VfDev& p, VfShared& s, int b, i
   __syncthreads();
 }
 
-// Pass `pass` (from 0 on) over residuals: the walk goes on with the weights of the pass before.
-template <typename T>
-__global__ __launch_bounds__(BLOCK) void k_verify_rest(VfDev p, int pass) {
+// Pass `pass`; FIRST: pass 0, which joins the rows' sums. NT threads.
+template <typename T, bool FIRST>
+__global__ __launch_bounds__(FIRST ? VF_NT : BLOCK) void k_verify_pass(VfDev p, int pass) {
+  constexpr int NT = FIRST ? VF_NT : BLOCK;
   __shared__ VfShared s;
   const int chunk = blockIdx.x, b = blockIdx.y;
   const bool first = chunk == 0;
-  VfState* now = p.state + (long long)((pass + 1) & 1) * p.B + b;
-  if (p.state[(long long)(pass & 1) * p.B + b].done) {
-    if (first && threadIdx.x == 0) *now = p.state[(long long)(pass & 1) * p.B + b];
-    return;
-  }
-  load_state(p, s, b, pass);
   const double it = inv_temp(p, b);
-  if (pass > 0) {
-    const double* bins = rest_of(p, (pass - 1) & 1, b);
-    double left = 0.0;
-    for (int k = threadIdx.x; k < p.chunks; k += BLOCK) left += bins[k];
-    left = block_sum_d<BLOCK>(left, s.red);
-    if (threadIdx.x == 0) s.st.left = left;
-    walk(p, s, b, it, first);
-    if (s.st.done) {
+  VfState* now = p.state + (long long)((pass + 1) & 1) * p.B + b;
+  if constexpr (FIRST) {
+    join_rows<T>(p, s, b, it, first);
+    walk(p, s, b, it, 0, first);
+  } else {
+    const VfState* was = p.state + (long long)(pass & 1) * p.B + b;
+    const int src = (pass - 1) & 1;
+    if (was->stage != WAIT_REST) {
       if (first && threadIdx.x == 0) {
-        *now = s.st;
-        now->done = 2 + ((pass - 1) & 1);
+        *now = *was;
+        if (was->stage == WAIT_DRAW) now->stage = DONE + src;
       }
       return;
     }
+    load_state(p, s, b, pass);
+    join_bins<NT>(p, s, bins_of(p, src, b));
+    walk(p, s, b, it, src, first);
   }
-  double v = 0.0, w[8];
-#pragma unroll
-  for (int g = 0; g < VF_CH / (8 * BLOCK); ++g) {
-    const int i = chunk * VF_CH + (g * BLOCK + (int)threadIdx.x) * 8;
-    if (i < p.V) {
-      rest8<T>(p, s, b, REST_Q, it, i, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v += w[j];
-    }
-  }
-  v = block_sum_d<BLOCK>(v, s.red);
-  if (threadIdx.x == 0) {
-    rest_of(p, pass & 1, b)[chunk] = v;
-    if (first) *now = s.st;
-  }
+  if (first && threadIdx.x == 0) *now = s.st;
+  if (s.st.stage >= DONE) return;
+  const VfBin v = bin_block<T, NT>(p, s, b, it, chunk);
+  if (threadIdx.x == 0) bins_of(p, pass & 1, b)[chunk] = v;
 }
 
 template <typename T>
 __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
   __shared__ VfShared s;
   const int b = blockIdx.x;
+  const double it = inv_temp(p, b);
   load_state(p, s, b, passes);
-  to_the_end<T>(p, s, b, inv_temp(p, b), rest_of(p, s.st.done > 1 ? s.st.done - 2 : (passes - 1) & 1, b));
+  int src = (passes - 1) & 1;
+  // at most one round per node and one more per row: each consumes a child or settles a row's sum
+  while (s.st.stage < DONE) {
+    if (s.st.stage == WAIT_DRAW) {
+      __syncthreads();
+      if (threadIdx.x == 0) s.st.stage = DONE + src;
+      __syncthreads();
+      break;
+    }
+    join_bins<VF_NT>(p, s, bins_of(p, src, b));
+    walk(p, s, b, it, src, true);
+    if (s.st.stage >= DONE) break;
+    src = 2;
+    for (int k = 0; k < p.chunks; ++k) {
+      const VfBin v = bin_block<T, VF_NT>(p, s, b, it, k);
+      if (threadIdx.x == 0) bins_of(p, 2, b)[k] = v;
+    }
+    __threadfence_block();
+    __syncthreads();
+  }
+  finish<T>(p, s, b, it);
 }
 
 template <typename T>
@@ -684,11 +648,11 @@ pi_status launch_verify(pi_ctx* c, const VfDev& p) {
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, 1>, dim3((p.chunks + NWAVES - 1) / NWAVES, p.N, p.B), 0, p));
   else
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, NWAVES>, dim3(p.chunks, p.N, p.B), 0, p));
-  const bool all = p.q == nullptr || p.N == 1 || p.chunks <= VF_OWN_CHUNKS;
-  PI_HIP(c, launch_kb(c, 0, k_verify_walk<T>, dim3(p.B), VF_NT, 0, p, all));
-  if (all) return PI_OK;
-  const int passes = std::min(VF_RESTS, p.N - 1);
-  for (int i = 0; i < passes; ++i) PI_HIP(c, launch_k(c, 0, k_verify_rest<T>, dim3(p.chunks, p.B), 0, p, i));
+  // A pass that finds nothing to do costs 2 us; one that the last kernel does by itself some 20 us
+  // at 131072 tokens and 5 at 32000. Without a q one is enough but for tests too near to call.
+  const int passes = p.q == nullptr ? 1 : std::min(p.chunks > 16 ? 4 : 2, std::max(1, p.N - 1));
+  PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, true>, dim3(p.chunks, p.B), VF_NT, 0, p, 0));
+  for (int i = 1; i < passes; ++i) PI_HIP(c, launch_k(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), 0, p, i));
   PI_HIP(c, launch_kb(c, 0, k_verify_end<T>, dim3(p.B), VF_NT, 0, p, passes));
   return PI_OK;
 }
@@ -707,8 +671,8 @@ pi_status pi_verifier_create(pi_ctx* ctx, int32_t vocab, int32_t max_batch, int3
   const int chunks = (vocab + VF_CH - 1) / VF_CH;
   const size_t rows = (size_t)max_batch * max_nodes;
   const size_t o_rows = sizeof(VfPart) * rows * chunks, o_state = o_rows + sizeof(VfRow) * rows,
-               o_rest = o_state + 2 * sizeof(VfState) * max_batch,
-               bytes = o_rest + 3 * sizeof(double) * max_batch * chunks;
+               o_bins = o_state + 2 * sizeof(VfState) * max_batch,
+               bytes = o_bins + 3 * sizeof(VfBin) * max_batch * chunks;
   PI_HIP(ctx, hipSetDevice(ctx->device));
   uint8_t* ws = nullptr;
   if (hipMalloc(reinterpret_cast<void**>(&ws), bytes) != hipSuccess) {
@@ -717,7 +681,7 @@ pi_status pi_verifier_create(pi_ctx* ctx, int32_t vocab, int32_t max_batch, int3
   }
   pi_verifier* v = new (std::nothrow) pi_verifier{
       ctx, vocab, max_batch, max_nodes, chunks, ws, reinterpret_cast<VfPart*>(ws), reinterpret_cast<VfRow*>(ws + o_rows),
-      reinterpret_cast<VfState*>(ws + o_state), reinterpret_cast<double*>(ws + o_rest)};
+      reinterpret_cast<VfState*>(ws + o_state), reinterpret_cast<VfBin*>(ws + o_bins)};
   if (v == nullptr) {
     (void)hipFree(ws);
     return fail(ctx, PI_ERR_OOM, "host allocation failed");
@@ -755,7 +719,7 @@ pi_status pi_verify(pi_ctx* ctx, pi_verifier* ver, const pi_verify_args* args) {
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const VfDev p{a.logits, a.q, a.logits_batch, a.logits_node, a.q_batch, a.q_node, a.tokens, a.parents, a.u, a.u_next,
                 a.temperature, a.nodes, a.out, a.n, a.B, a.N, ver->vocab, ver->chunks, ver->part, ver->rows, ver->state,
-                ver->rest};
+                ver->bins};
   switch (a.dtype) {
     case PI_T_F32: return launch_verify<float>(ctx, p);
     case PI_T_F16: return launch_verify<half_t>(ctx, p);
