@@ -44,6 +44,7 @@ struct pi_ctx {
   half_t* zlo = nullptr;
   half_t* a16 = nullptr;        // [32 or 64][lda] activations at compacted positions
   int lda = 0;
+  int32_t* lin_part = nullptr;  // sums of the 8-bit product's ranges of K (pi_linear_create)
   std::string err;
   // cached graph of one stack step, captured on a private stream (the caller's stream may be
   // the null stream, which cannot be captured) and launched on the caller's stream

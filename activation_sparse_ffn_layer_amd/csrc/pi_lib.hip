@@ -1031,6 +1031,7 @@ void pi_ctx_destroy(pi_ctx* ctx) {
   if (ctx->cap_stream != nullptr) (void)hipStreamDestroy(ctx->cap_stream);
   for (hipEvent_t e : ctx->ev) (void)hipEventDestroy(e);
   if (ctx->ws != nullptr) (void)hipFree(ctx->ws);
+  if (ctx->lin_part != nullptr) (void)hipFree(ctx->lin_part);
   delete ctx;
 }
 

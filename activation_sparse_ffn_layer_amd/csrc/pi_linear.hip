@@ -24,6 +24,7 @@ struct LinDev {
   const int8_t *x, *w;
   const float *xs, *ws, *bias;
   void* y;
+  int32_t* part;  // sums of ranges of K
   long long x_stride, w_stride, y_stride;
   int M, N, K;
 };
@@ -63,15 +64,18 @@ __device__ __forceinline__ void put4(const LinDev& p, int m, int n0, const float
       if (n0 + i < p.N) y[i] = (T)v[i];
   }
 }
-template <typename T>
-__device__ __forceinline__ void put4(const LinDev& p, int m, int n0, i32x4 s, bool wide) {
-  float ws[4], bias[4];
+__device__ __forceinline__ void scales4(const LinDev& p, int n0, float (&ws)[4], float (&bias)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = min(n0 + i, p.N - 1);
     ws[i] = p.ws[n];
     bias[i] = p.bias != nullptr ? p.bias[n] : 0.f;
   }
+}
+template <typename T>
+__device__ __forceinline__ void put4(const LinDev& p, int m, int n0, i32x4 s, bool wide) {
+  float ws[4], bias[4];
+  scales4(p, n0, ws, bias);
   put4<T>(p, m, n0, ws, bias, s, wide);
 }
 
@@ -155,15 +159,21 @@ __global__ __launch_bounds__(64 * LR_WAVES) void k_q8_rows(LinDev p, bool wide) 
 }
 
 // ---------------------------------------------------------------------------------------
-// Many tokens: bound by the matrix cores. Four waves own a square tile of 64 FB weight rows and
-// tokens, staged in LDS 64 bytes of K at a time in three stages. In step s the products of
-// stage s run, with the operands of the next 32 bytes of K read ahead (also across the step's
-// barrier: stage s + 1 is complete), stage s + 2 is written from registers, and those are
-// loaded anew, two steps before they are needed. A wave's quarter of the tile is FB x FB blocks
-// of 32 x 32, so LDS is read 2 FB rows for FB^2 products.
+// More tokens: four waves own a square tile of 64 FB weight rows and tokens, staged in LDS 128
+// bytes of K at a time in two stages. A step's products take the stage 32 bytes at a time, with
+// the operands of the next 32 bytes read ahead. Its one barrier stands before the last of the
+// four: by then the stage has been read to its end and the other one is written, whose first
+// operands the last products cover; and the stage just read is free for what the registers
+// hold. So no wave waits for an LDS read or a load that it has just issued.
+//   FB = 4: bound by the matrix cores (a wave's 128 x 128 take 8 reads of LDS for 16 products).
+//   FB = 2: where tiles of 256 would leave CUs idle. With SPLIT, for few tiles, each is cut in
+//   `splits` ranges of K, whose whole-number sums k_q8_join adds: bound by the loads' latency and
+//   the weights' bytes.
+// Row r's piece c of 16 bytes lies at c ^ (r / 2 % 8), so that 16 rows' reads of one piece meet
+// all 64 banks.
 // ---------------------------------------------------------------------------------------
-constexpr int LT_K = 64, LT_P = LT_K + 16;  // K bytes per stage; LDS row pitch (bytes)
-template <int FB> constexpr size_t tile_lds() { return (size_t)3 * 2 * 64 * FB * LT_P; }
+constexpr int LT_K = 128;  // K bytes per stage, which is a row of LDS
+template <int FB> constexpr size_t tile_lds() { return (size_t)2 * 2 * 64 * FB * LT_K; }
 
 // The tile of workgroup id: the XCDs (id % 8) take equal runs of tiles, in an order that
 // walks 8 tiles of tokens, then the weight rows, so that an XCD's tiles in flight share rows.
@@ -175,39 +185,46 @@ __device__ __forceinline__ void tile_of(int id, int tn, int tm, int* n, int* m) 
   *n = r / high;
 }
 
-template <typename T, int FB>
+template <typename T, int FB, bool SPLIT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(FB == 4 ? 1 : 2, FB == 4 ? 1 : 2)))
 void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
-  constexpr int TL = 64 * FB, R = 2 * FB, STAGE = 2 * TL * LT_P;  // R loads of 64 rows for both operands
+  constexpr int TL = 64 * FB, R = 4 * FB, STAGE = 2 * TL * LT_K;  // R loads of 32 rows for both operands
+  constexpr int SETS = FB == 4 ? 1 : 2;                           // stages held in registers
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, half = lane >> 5, l32 = lane & 31;
   int nt, mt;
   tile_of(blockIdx.x, tn, tm, &nt, &mt);
   const int n0 = nt * TL, m0 = mt * TL;
-  const int lr = threadIdx.x >> 2, lk = 16 * (threadIdx.x & 3);  // row of a pass of 64, byte in the row
+  const int lr = threadIdx.x >> 3, lk = 16 * (threadIdx.x & 7);  // row of a pass of 32, byte in the row
   const int wrows = min(TL, p.N - n0), xrows = min(TL, p.M - m0);
   const auto wb = row_buffer(p.w, n0, wrows, p.w_stride, p.K), xb = row_buffer(p.x, m0, xrows, p.x_stride, p.K);
   uint32_t at[R];  // rows past the last read it again
 #pragma unroll
-  for (int i = 0; i < FB; ++i) {
-    at[i] = (uint32_t)(min(lr + 64 * i, wrows - 1) * (int)p.w_stride + lk);
-    at[FB + i] = (uint32_t)(min(lr + 64 * i, xrows - 1) * (int)p.x_stride + lk);
+  for (int i = 0; i < R / 2; ++i) {
+    at[i] = (uint32_t)(min(lr + 32 * i, wrows - 1) * (int)p.w_stride + lk);
+    at[R / 2 + i] = (uint32_t)(min(lr + 32 * i, xrows - 1) * (int)p.x_stride + lk);
   }
-  u32x4 r[2][R];
-  auto load = [&](int set, int i, int k0) {
-    r[set][i] = buffer16<0>(i < FB ? wb : xb, k0 + lk < p.K ? at[i] + k0 : OOB);
+  const int all = (p.K + LT_K - 1) / LT_K;
+  const int first = SPLIT ? (int)((long long)all * blockIdx.y / gridDim.y) : 0;
+  const int steps = (SPLIT ? (int)((long long)all * (blockIdx.y + 1) / gridDim.y) : all) - first;
+  u32x4 r[SETS][R];
+  auto load = [&](int set, int i, int step) {
+    const int k0 = (first + step) * LT_K;
+    r[set][i] = buffer16<0>(i < R / 2 ? wb : xb, step < steps && k0 + lk < p.K ? at[i] + k0 : OOB);
   };
-  uint8_t* const put = lds + lr * LT_P + lk;
-  auto store = [&](int set, int i, int stage) { *reinterpret_cast<u32x4*>(put + stage + 64 * i * LT_P) = r[set][i]; };
+  uint8_t* const put = lds + lr * LT_K + (lk ^ (lr >> 1 & 7) * 16);
+  auto store = [&](int set, int i, int stage) { *reinterpret_cast<u32x4*>(put + stage * STAGE + 32 * i * LT_K) = r[set][i]; };
   const int wn = 32 * FB * (wave & 1), wm = 32 * FB * (wave >> 1);
-  const uint8_t* const ga = lds + (wn + l32) * LT_P + 16 * half;
-  const uint8_t* const gb = lds + (TL + wm + l32) * LT_P + 16 * half;
+  const uint8_t* const ga = lds + (wn + l32) * LT_K;
+  const uint8_t* const gb = lds + (TL + wm + l32) * LT_K;
+  const int piece = (half ^ (l32 >> 1 & 7)) * 16;  // of the first 32 bytes; of the k-th 32 at ^ 32 k
   i32x4 a[2][FB], b[2][FB];
-  auto fetch = [&](int set, int at_) {
+  auto fetch = [&](int set, int stage, int k) {
+    const int o = stage * STAGE + (piece ^ (32 * k));
 #pragma unroll
     for (int i = 0; i < FB; ++i) {
-      a[set][i] = *reinterpret_cast<const i32x4*>(ga + at_ + 32 * i * LT_P);
-      b[set][i] = *reinterpret_cast<const i32x4*>(gb + at_ + 32 * i * LT_P);
+      a[set][i] = *reinterpret_cast<const i32x4*>(ga + o + 32 * i * LT_K);
+      b[set][i] = *reinterpret_cast<const i32x4*>(gb + o + 32 * i * LT_K);
     }
   };
   i32x16 acc[FB][FB];
@@ -222,58 +239,73 @@ void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
       for (int j = 0; j < FB; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
   };
-  const int steps = (p.K + LT_K - 1) / LT_K;
+  // a quarter of a stage's writes, and of the loads into their registers
+  auto quarter = [&](int q, int stage, int set, int step) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+    for (int i = q * (R / 4); i < (q + 1) * (R / 4); ++i) {
+      store(set, i, stage);
+      load(set, i, step);
+    }
+  };
+  // Order of a quarter: reads of LDS and products in turn, then writes and loads between products.
+  auto order = [&]() {
+    if constexpr (FB == 4) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) load(h, i, h * LT_K);
+      for (int i = 0; i < 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // read of LDS
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // product
+      }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // write to LDS
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < R; ++i) store(h, i, h * STAGE);
-#pragma unroll
-    for (int i = 0; i < R; ++i) load(h, i, (h + 2) * LT_K);  // zeros past K
-  }
-  __syncthreads();
-  int s0 = 0, s1 = STAGE, s2 = 2 * STAGE;  // stages s, s + 1, s + 2
-  fetch(0, 0);
-  // one step; registers h hold stage s + 2
-  auto step = [&](int s, int h) {
-    fetch(1, s0 + 32);
-#pragma unroll
-    for (int i = 0; i < R / 2; ++i) store(h, i, s2);
-    products(0);
-    fetch(0, s1);
-#pragma unroll
-    for (int i = R / 2; i < R; ++i) store(h, i, s2);
-#pragma unroll
-    for (int i = 0; i < R; ++i) load(h, i, (s + 4) * LT_K);
-    products(1);
-    if constexpr (FB == 4) {  // the memory operations between the products, so that neither waits for the other
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // read of LDS
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // product
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // write to LDS
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (g == 1) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);  // load
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       }
     }
+  };
+#pragma unroll
+  for (int i = 0; i < R; ++i) load(0, i, 0);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    store(0, i, 0);
+    load(0, i, SETS == 1 ? 1 : 2);
+  }
+  if constexpr (SETS == 2) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) load(1, i, 1);
+  }
+  __syncthreads();
+  fetch(0, 0, 0);
+  // the last quarter of stage 1's writes is where a step before would have put the first
+  quarter(0, 1, SETS - 1, SETS == 1 ? 2 : 3);
+  // Step s from stage h; the other stage gets step s + 1 in the first three quarters (its first
+  // quarter is written already), and this one the first quarter of step s + 2 in the last.
+  auto step = [&](int s, int h) {
+    constexpr int D = SETS;  // a register is loaded D steps after the one it held
+    const int next = SETS == 1 ? 0 : h ^ 1, then = SETS == 1 ? 0 : h;
+    fetch(1, h, 1);
+    quarter(1, h ^ 1, next, s + 1 + D);
+    products(0);
+    order();
+    fetch(0, h, 2);
+    quarter(2, h ^ 1, next, s + 1 + D);
+    products(1);
+    order();
+    fetch(1, h, 3);
+    quarter(3, h ^ 1, next, s + 1 + D);
+    products(0);
+    order();
     __syncthreads();
-    const int t = s0;
-    s0 = s1;
-    s1 = s2;
-    s2 = t;
+    fetch(0, h ^ 1, 0);
+    quarter(0, h, then, s + 2 + D);
+    products(1);
+    order();
   };
   int s = 0;
   for (; s + 1 < steps; s += 2) {
@@ -281,6 +313,25 @@ void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
     step(s + 1, 1);
   }
   if (s < steps) step(s, 0);
+  if constexpr (SPLIT) {
+    const int Np = (p.N + 3) & ~3;
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int m = m0 + wm + 32 * j + l32;
+      if (m < p.M) {
+        int32_t* o = p.part + ((long long)blockIdx.y * p.M + m) * Np;
+#pragma unroll
+        for (int i = 0; i < FB; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = n0 + wn + 32 * i + 8 * q + 4 * half;
+            if (n < p.N)
+              *reinterpret_cast<i32x4*>(o + n) = (i32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          }
+      }
+    }
+    return;
+  }
   const bool whole = wide && n0 + TL <= p.N && m0 + TL <= p.M;
 #pragma unroll
   for (int i = 0; i < FB; ++i)
@@ -288,12 +339,7 @@ void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
     for (int q = 0; q < 4; ++q) {
       const int n = n0 + wn + 32 * i + 8 * q + 4 * half;
       float ws[4], bias[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = min(n + e, p.N - 1);
-        ws[e] = p.ws[c];
-        bias[e] = p.bias != nullptr ? p.bias[c] : 0.f;
-      }
+      scales4(p, n, ws, bias);
 #pragma unroll
       for (int j = 0; j < FB; ++j) {
         const i32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
@@ -303,31 +349,53 @@ void k_q8_tile(LinDev p, int tn, int tm, bool wide) {
     }
 }
 
-template <typename T, int FB>
-pi_status launch_tile(pi_ctx* c, const LinDev& p, bool wide) {
+// The sums of a tile's ranges of K, 4 channels of a token per thread.
+template <typename T>
+__global__ __launch_bounds__(BLOCK) void k_q8_join(LinDev p, int splits, bool wide) {
+  const int n = 4 * (blockIdx.x * BLOCK + threadIdx.x), m = blockIdx.y;
+  if (n >= p.N) return;
+  const int Np = (p.N + 3) & ~3;
+  const int32_t* o = p.part + (long long)m * Np + n;
+  const long long next = (long long)p.M * Np;
+  i32x4 s = {0, 0, 0, 0};
+  for (int i0 = 0; i0 < splits; i0 += 8) {
+    i32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const i32x4*>(o + min(i0 + i, splits - 1) * next);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i0 + i < splits) s += v[i];
+  }
+  put4<T>(p, m, n, s, wide);
+}
+
+template <typename T, int FB, bool SPLIT>
+pi_status launch_tile(pi_ctx* c, const LinDev& p, bool wide, int splits) {
   const int tn = (p.N + 64 * FB - 1) / (64 * FB), tm = (p.M + 64 * FB - 1) / (64 * FB);
-  PI_HIP(c, allow_lds(k_q8_tile<T, FB>, tile_lds<FB>()));
-  PI_HIP(c, launch_kb(c, 0, k_q8_tile<T, FB>, dim3((unsigned)(tn * tm)), 256, tile_lds<FB>(), p, tn, tm, wide));
+  PI_HIP(c, allow_lds(k_q8_tile<T, FB, SPLIT>, tile_lds<FB>()));
+  PI_HIP(c, launch_kb(c, 0, k_q8_tile<T, FB, SPLIT>, dim3((unsigned)(tn * tm), splits), 256, tile_lds<FB>(), p, tn, tm, wide));
+  if (SPLIT) PI_HIP(c, launch_k(c, 0, k_q8_join<T>, dim3(((p.N + 3) / 4 + BLOCK - 1) / BLOCK, p.M), 0, p, splits, wide));
   return PI_OK;
+}
+
+// Ranges of K that tiles of 128 are cut in: as many workgroups as two per CU take at once, each
+// of four steps at least.
+int split_count(int cus, int tiles, int K) {
+  return std::max(1, std::min(2 * cus / tiles, (K + LT_K - 1) / LT_K / 4));
 }
 
 template <typename T>
 pi_status launch_linear(pi_ctx* c, const LinDev& p) {
   // 4 outputs in one store where every row starts at such a boundary
   const bool wide = p.y_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-  if (p.M > 256) {
-    const long long big = (long long)((p.N + 255) / 256) * ((p.M + 255) / 256);
-    return big >= c->cus ? launch_tile<T, 4>(c, p, wide) : launch_tile<T, 2>(c, p, wide);
+  if (p.M <= 16) {
+    PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 2>, dim3((p.N + 31) / 32), 64 * LR_WAVES, 0, p, wide));
+    return PI_OK;
   }
-  const int mb = std::min(4, (p.M + 15) / 16);
-  const dim3 g((p.N + 31) / 32, (p.M + 16 * mb - 1) / (16 * mb));
-  switch (mb) {
-    case 1: PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 2>, g, 64 * LR_WAVES, 0, p, wide)); break;
-    case 2: PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 2, 2>, g, 64 * LR_WAVES, 0, p, wide)); break;
-    case 3: PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 3, 2>, g, 64 * LR_WAVES, 0, p, wide)); break;
-    default: PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 4, 2>, g, 64 * LR_WAVES, 0, p, wide));
-  }
-  return PI_OK;
+  const long long big = (long long)((p.N + 255) / 256) * ((p.M + 255) / 256);
+  if (big >= c->cus) return launch_tile<T, 4, false>(c, p, wide, 1);
+  const int splits = split_count(c->cus, ((p.N + 127) / 128) * ((p.M + 127) / 128), p.K);
+  return splits > 1 ? launch_tile<T, 2, true>(c, p, wide, splits) : launch_tile<T, 2, false>(c, p, wide, 1);
 }
 
 }  // namespace
@@ -348,6 +416,16 @@ pi_status pi_linear_create(pi_ctx* ctx, const pi_linear_desc* desc, pi_linear** 
   PI_TRY(check_dev_ptr(ctx, d.w, "w"));
   PI_TRY(check_dev_ptr(ctx, d.w_scale, "w_scale"));
   PI_TRY(check_dev_ptr(ctx, d.bias, "bias", true));
+  // one buffer per context: its calls run one after another
+  if (d.max_tokens > 16 && ctx->lin_part == nullptr) {
+    PI_HIP(ctx, hipSetDevice(ctx->device));
+    const size_t bytes = (size_t)2 * ctx->cus * 128 * 128 * 4;
+    if (hipMalloc(reinterpret_cast<void**>(&ctx->lin_part), bytes) != hipSuccess) {
+      (void)hipGetLastError();
+      ctx->lin_part = nullptr;
+      return fail(ctx, PI_ERR_OOM, "product scratch of %zu bytes", bytes);
+    }
+  }
   pi_linear* l = new (std::nothrow) pi_linear{ctx, d};
   if (l == nullptr) return fail(ctx, PI_ERR_OOM, "host allocation failed");
   *out = l;
@@ -376,7 +454,7 @@ pi_status pi_linear_q8(pi_ctx* ctx, pi_linear* lin, const int8_t* x, int64_t x_s
   if ((reinterpret_cast<uintptr_t>(x_scale) & 3u) || (reinterpret_cast<uintptr_t>(y) & (y_dtype == PI_T_F32 ? 3u : 1u)))
     return fail(ctx, PI_ERR_INVALID, "x_scale or y is not aligned to its elements");
   PI_HIP(ctx, hipSetDevice(ctx->device));
-  const LinDev p{x, d.w, x_scale, d.w_scale, d.bias, y, M > 1 ? x_stride : 0, d.w_stride, y_stride, M, d.N, d.K};
+  const LinDev p{x, d.w, x_scale, d.w_scale, d.bias, y, ctx->lin_part, M > 1 ? x_stride : 0, d.w_stride, y_stride, M, d.N, d.K};
   switch (y_dtype) {
     case PI_T_F32: return launch_linear<float>(ctx, p);
     case PI_T_F16: return launch_linear<half_t>(ctx, p);
