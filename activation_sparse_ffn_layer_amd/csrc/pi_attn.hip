@@ -27,6 +27,7 @@ struct pi_attn {
   uint8_t* ws;
   float* part;      // [slots][kv heads][rows][DP]
   float* ml;        // [slots][kv heads][rows][2]: maximum (log2 domain) and sum
+  int32_t* self;    // 0, 1, ..: the page table of calls without one
 };
 
 namespace {
@@ -142,7 +143,7 @@ constexpr size_t attn_lds() {
 // WQ waves along the query rows (32 each), WK along a tile's keys (32 KB each). With WQ == 1 a
 // wave loads and reads its own keys only and the tile loop has no barrier.
 template <typename T, int DP, int WQ, int WK, int KB>
-__global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
+__global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tree_attn(AttnDev a) {
   constexpr int KW = 32 * KB, KT = KW * WK, NT = 64 * WQ * WK;
   constexpr bool OWN = WQ == 1;                          // tiles private to a wave
   constexpr int LPR = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // lanes that load one row
@@ -187,36 +188,63 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
   const int lr = lt / LPR + (OWN ? wk * KW : 0), lc = lt % LPR;
   const bool piece_in = lc * 8 < a.D;
   uint8_t* const ks = smem + (OWN ? wk * KW * (KP + VP) : 0);
-  const long long khead = (long long)hk * a.c.head_stride, nhead = (long long)hk * a.kv_head + (long long)b * a.kv_batch;
+  const long long nhead = (long long)hk * a.kv_head + (long long)b * a.kv_batch;
   // A tile's rows are loaded in two steps, their pages' numbers one tile ahead of the rows. What is
-  // not there is read from a zero in memory: a select after the load would wait for it.
+  // not there is read from zeros in memory: a select after the load would wait for it. `ready`
+  // keeps the compiler from computing an address behind a branch.
   constexpr int SETS = OWN ? 1 : 2;
   u32x4 kr[SETS][PASS], vr[SETS][PASS];
   int pg[PASS];
+  const int32_t* const pages = a.c.table + (long long)b * a.c.table_stride;
+  // global pointers by type: a generic load counts as a read of LDS too, and holds those up
+  typedef const __attribute__((address_space(1))) uint8_t* gp;
+  const gp zero = (gp)(const uint8_t*)&attn_zero;
+  const gp kc = (gp)(static_cast<const uint8_t*>(a.c.k) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
+  const gp vc = (gp)(static_cast<const uint8_t*>(a.c.v) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
+  const gp kn = (gp)(a.kn + 2 * (nhead + lc * 8)), vn = (gp)(a.vn + 2 * (nhead + lc * 8));
+  const uint32_t token_bytes = 2 * (uint32_t)a.c.token_stride;
+  const long long page_bytes = 2 * a.c.page_stride, node_bytes = 2 * a.kv_node;
+  const uint32_t npages = (uint32_t)a.c.pages;
+  const PageDiv div = a.c.div;
+  auto ready = [](gp p) {
+    asm("" : "+v"(p));
+    return p;
+  };
   auto ids = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < PASS; ++i) {
-      const int p = tile * KT + lr + i * RPP;
       uint32_t off;
-      const uint32_t n = page_of(a.c.div, (uint32_t)min(p, max(len - 1, 0)), &off);
-      pg[i] = a.c.table == nullptr ? b : a.c.table[(long long)b * a.c.table_stride + n];
+      pg[i] = pages[page_of(div, (uint32_t)min(tile * KT + lr + i * RPP, max(len - 1, 0)), &off)];
     }
   };
   auto load = [&](int tile, int set) {
+    const int p0 = tile * KT + lr;
+    gp kp[PASS], vp[PASS];
+    const bool in = piece_in & (tile < ch.t1);
 #pragma unroll
     for (int i = 0; i < PASS; ++i) {
-      const int p = tile * KT + lr + i * RPP;
       uint32_t off;
-      page_of(a.c.div, (uint32_t)p, &off);
-      const bool old = p < len;
-      const bool ok = piece_in && tile < ch.t1 && (old ? (unsigned)pg[i] < (unsigned)a.c.pages : p < total);
-      const long long at = lc * 8 + (old ? (long long)pg[i] * a.c.page_stride + (long long)off * a.c.token_stride + khead
-                                         : (long long)(p - len) * a.kv_node + nhead);
-      const uint8_t* kp = (old ? static_cast<const uint8_t*>(a.c.k) : a.kn) + 2 * at;
-      const uint8_t* vp = (old ? static_cast<const uint8_t*>(a.c.v) : a.vn) + 2 * at;
-      const uint8_t* zero = reinterpret_cast<const uint8_t*>(&attn_zero);
-      kr[set][i] = ld16(ok ? kp : zero);
-      vr[set][i] = ld16(ok ? vp : zero);
+      page_of(div, (uint32_t)(p0 + i * RPP), &off);
+      const bool ok = in & (p0 + i * RPP < len) & ((uint32_t)pg[i] < npages);
+      const long long at = (long long)pg[i] * page_bytes + (unsigned long long)off * token_bytes;
+      const gp k = ready(kc + at), v = ready(vc + at);
+      kp[i] = ok ? k : zero;
+      vp[i] = ok ? v : zero;
+    }
+    if (tile * KT + KT > len) {  // new nodes among the tile's rows
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        const int j = p0 + i * RPP - len;
+        const bool ok = in & (j >= 0) & (j < a.N);
+        const gp k = ready(kn + j * node_bytes), v = ready(vn + j * node_bytes);
+        kp[i] = ok ? k : kp[i];
+        vp[i] = ok ? v : vp[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      kr[set][i] = *(const __attribute__((address_space(1))) u32x4*)kp[i];
+      vr[set][i] = *(const __attribute__((address_space(1))) u32x4*)vp[i];
     }
   };
   // a stage is K rows, then V rows
@@ -367,22 +395,25 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
   }
 
   l = swap_add(l);
+  // the infinities and NaN of the new nodes' values that row r sees, for its columns d..d+3
+  auto odd4 = [&](int r, int d, f32x4* v) {
+    if (!s_odd || d >= a.D) return;
+    const int rn = r / a.G;
+    const uint64_t w = a.tree != nullptr ? a.tree[(long long)b * a.N + rn] : (2ull << rn) - 1;
+    for (int j = 0; j < a.N; ++j)
+      if (((w >> j) & 1) && len + j >= ch.t0 * KT && len + j < ch.t1 * KT) {
+        const T* x = reinterpret_cast<const T*>(a.vn) + nhead + (long long)j * a.kv_node + d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = (float)x[i];
+          if (!(fabsf(y) < __builtin_inff())) (*v)[i] += y;
+        }
+      }
+  };
   // 4 columns d..d+3 of a query row: the output itself when the sequence is one chunk
   auto put = [&](int r, int d, f32x4 v, float mm, float ll) {
     if (d >= a.D) return;
-    if (s_odd) {
-      const int rn = r / a.G;
-      uint64_t w = a.tree != nullptr ? a.tree[(long long)b * a.N + rn] : (2ull << rn) - 1;
-      for (int j = 0; j < a.N; ++j)
-        if (((w >> j) & 1) && len + j >= ch.t0 * KT && len + j < ch.t1 * KT) {
-          const T* x = reinterpret_cast<const T*>(a.vn) + nhead + (long long)j * a.kv_node + d;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float y = (float)x[i];
-            if (!(fabsf(y) < __builtin_inff())) v[i] += y;
-          }
-        }
-    }
+    if constexpr (WK > 1) odd4(r, d, &v);
     if (ch.count == 1) {
       const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
       T* o4 = reinterpret_cast<T*>(a.out) + (long long)b * a.out_batch + (long long)(r / a.G) * a.out_node +
@@ -402,6 +433,17 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_tree_attn(AttnDev a) {
   };
   if constexpr (WK == 1) {
     if (!live) return;
+    if (s_odd) {
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          f32x4 v = (f32x4){o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
+          odd4(row, 32 * i + acc_row(r, half), &v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][r + e] = v[e];
+        }
+    }
 #pragma unroll
     for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -595,12 +637,19 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
   PI_HIP(ctx, hipSetDevice(ctx->device));
   uint8_t* ws = nullptr;
   const size_t ob = rows * DP * 4, mb = rows * 2 * 4;
-  if (hipMalloc(reinterpret_cast<void**>(&ws), ob + mb) != hipSuccess) {
+  if (hipMalloc(reinterpret_cast<void**>(&ws), ob + mb + (size_t)max_batch * 4) != hipSuccess) {
     (void)hipGetLastError();
     return fail(ctx, PI_ERR_OOM, "attention scratch of %zu bytes", ob + mb);
   }
+  int32_t* self = reinterpret_cast<int32_t*>(ws + ob + mb);
+  std::vector<int32_t> id(max_batch);
+  for (int i = 0; i < max_batch; ++i) id[i] = i;
+  if (hipMemcpy(self, id.data(), id.size() * 4, hipMemcpyHostToDevice) != hipSuccess) {
+    (void)hipFree(ws);
+    return fail(ctx, PI_ERR_HIP, "filling the attention scratch failed");
+  }
   pi_attn* a = new (std::nothrow) pi_attn{ctx, kv, heads, max_batch, max_nodes, scale, ws, reinterpret_cast<float*>(ws),
-                                          reinterpret_cast<float*>(ws + ob)};
+                                          reinterpret_cast<float*>(ws + ob), self};
   if (a == nullptr) {
     (void)hipFree(ws);
     return fail(ctx, PI_ERR_OOM, "host allocation failed");
@@ -634,7 +683,12 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const int HK = kv->desc.heads, G = attn->heads / HK;
   const AttnPlan p = attn_plan(ctx->cus, HK, a.N * G, a.B);
-  const AttnDev d{kv_dev(kv, a.table, a.table_stride, a.table_width), static_cast<const uint8_t*>(a.q),
+  KvDev c = kv_dev(kv, a.table, a.table_stride, a.table_width);
+  if (a.table == nullptr) {
+    c.table = attn->self;
+    c.table_stride = 1;
+  }
+  const AttnDev d{c, static_cast<const uint8_t*>(a.q),
                   static_cast<const uint8_t*>(a.k_new), static_cast<const uint8_t*>(a.v_new),
                   static_cast<uint8_t*>(a.out), a.tree, a.ctx_len, attn->part, attn->ml, a.q_batch, a.q_node, a.q_head,
                   a.kv_batch, a.kv_node, a.kv_head, a.out_batch, a.out_node, a.out_head, a.B, a.N, attn->heads, HK, G,
