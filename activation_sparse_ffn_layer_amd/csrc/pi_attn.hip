@@ -48,9 +48,10 @@ struct AttnDev {
 template <typename T> struct Mm;
 template <> struct Mm<half_t> {
   typedef half8_t v8;
-  // weights are carried times 2^14 (at most 16384), so that fp16 keeps its 11 bits down to 2^-28
-  // of the largest; below, a long cache's many small weights would round away together
-  static constexpr float SHIFT = 14.f;
+  // weights are carried times 2^10 and may grow by 2^5 beyond their base's (at most 2^15), so that
+  // fp16 keeps its 11 bits down to 2^-24 of that; below, a long cache's many small weights would
+  // round away together
+  static constexpr float SHIFT = 10.f, LAZY = 5.f;
   static constexpr uint32_t EXP = 0x7C00u;
   static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -58,7 +59,7 @@ template <> struct Mm<half_t> {
 };
 template <> struct Mm<bf16_t> {
   typedef bf8_t v8;
-  static constexpr float SHIFT = 0.f;
+  static constexpr float SHIFT = 0.f, LAZY = 8.f;
   static constexpr uint32_t EXP = 0x7F80u;
   static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -128,10 +129,10 @@ __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o)
 __device__ u32x4 attn_zero;  // zeros, never written
 
 // LDS of a workgroup: keys, then values, of one tile (two where tiles are shared by waves). A
-// row's pitch is past the power of two: 16 bytes for K, whose rows are read 16 bytes a lane, 32
-// bytes for V, whose transposing reads take 32 bytes from each of 4 rows.
+// row's pitch spreads what is read at once over the 64 banks: 16 rows of 16 bytes of K, and of V,
+// by its transposing reads, 4 rows of 64 bytes.
 template <int DP> constexpr int k_pitch() { return DP * 2 + 16; }
-template <int DP> constexpr int v_pitch() { return DP * 2 + 32; }
+template <int DP> constexpr int v_pitch() { return DP * 2 % 128 == 0 ? DP * 2 + 64 : DP * 2; }
 template <int DP, int WQ, int WK, int KB>
 constexpr size_t attn_lds() {
   const size_t kt = 32 * KB * WK;
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   const int b = ch.b;
   const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, half = lane >> 5, l32 = lane & 31;
   const int wq = wave / WK, wk = wave % WK;
-  const int len = kv_len(a.c, a.ctx_len, b), total = len + a.N;
+  const int len = kv_len(a.c, a.ctx_len, b);
 
   // this lane's query row
   const int row = (rt * WQ + wq) * 32 + l32;
@@ -194,7 +195,6 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   // keeps the compiler from computing an address behind a branch.
   constexpr int SETS = OWN ? 1 : 2;
   u32x4 kr[SETS][PASS], vr[SETS][PASS];
-  int pg[PASS];
   const int32_t* const pages = a.c.table + (long long)b * a.c.table_stride;
   // global pointers by type: a generic load counts as a read of LDS too, and holds those up
   typedef const __attribute__((address_space(1))) uint8_t* gp;
@@ -202,43 +202,54 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   const gp kc = (gp)(static_cast<const uint8_t*>(a.c.k) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
   const gp vc = (gp)(static_cast<const uint8_t*>(a.c.v) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
   const gp kn = (gp)(a.kn + 2 * (nhead + lc * 8)), vn = (gp)(a.vn + 2 * (nhead + lc * 8));
-  const uint32_t token_bytes = 2 * (uint32_t)a.c.token_stride;
-  const long long page_bytes = 2 * a.c.page_stride, node_bytes = 2 * a.kv_node;
+  const uint32_t page_units = (uint32_t)(a.c.page_stride >> 3), token_units = (uint32_t)(a.c.token_stride >> 3);  // 16 bytes
+  const long long node_bytes = 2 * a.kv_node;
   const uint32_t npages = (uint32_t)a.c.pages;
-  const PageDiv div = a.c.div;
   auto ready = [](gp p) {
     asm("" : "+v"(p));
     return p;
   };
-  auto ids = [&](int tile) {
+  // The place of each row of a tile: page of the sequence and offset in it, and the page's number in
+  // the cache. Tiles follow each other, so a place moves on by the quotient and rest of KT / page.
+  struct Place {
+    uint32_t n, off;
+    int id;
+  };
+  const uint32_t page = a.c.div.page, last = len > 0 ? (uint32_t)(len - 1) / page : 0;
+  const uint32_t kt_n = KT / page, kt_off = KT % page;
+  Place pl[OWN ? 1 : 2][PASS];  // of two tiles in turn
+  auto ids = [&](Place (&p)[PASS], const Place (&before)[PASS]) {
 #pragma unroll
     for (int i = 0; i < PASS; ++i) {
-      uint32_t off;
-      pg[i] = pages[page_of(div, (uint32_t)min(tile * KT + lr + i * RPP, max(len - 1, 0)), &off)];
+      uint32_t n = before[i].n + kt_n, off = before[i].off + kt_off;
+      const bool over = off >= page;
+      p[i].n = n + (over ? 1 : 0);
+      p[i].off = off - (over ? page : 0);
+      p[i].id = pages[min(p[i].n, last)];
     }
   };
-  auto load = [&](int tile, int set) {
-    const int p0 = tile * KT + lr;
+  auto load = [&](int tile, int set, const Place (&p)[PASS]) {
     gp kp[PASS], vp[PASS];
-    const bool in = piece_in & (tile < ch.t1);
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < PASS; ++i) {
-      uint32_t off;
-      page_of(div, (uint32_t)(p0 + i * RPP), &off);
-      const bool ok = in & (p0 + i * RPP < len) & ((uint32_t)pg[i] < npages);
-      const long long at = (long long)pg[i] * page_bytes + (unsigned long long)off * token_bytes;
-      const gp k = ready(kc + at), v = ready(vc + at);
-      kp[i] = ok ? k : zero;
-      vp[i] = ok ? v : zero;
+      const unsigned long long at = (unsigned long long)(uint32_t)p[i].id * page_units + (unsigned long long)p[i].off * token_units;
+      kp[i] = kc + (at << 4);
+      vp[i] = vc + (at << 4);
+      bad |= (uint32_t)p[i].id >= npages;
     }
-    if (tile * KT + KT > len) {  // new nodes among the tile's rows
+    if (tile * KT + KT > len || a.D != DP || __any(bad)) {  // not all rows are whole rows of the cache
+      const int p0 = tile * KT + lr;
+      const bool in = piece_in & (tile < ch.t1);
 #pragma unroll
       for (int i = 0; i < PASS; ++i) {
         const int j = p0 + i * RPP - len;
-        const bool ok = in & (j >= 0) & (j < a.N);
+        const bool old = in & (j < 0) & ((uint32_t)p[i].id < npages), fresh = in & (j >= 0) & (j < a.N);
         const gp k = ready(kn + j * node_bytes), v = ready(vn + j * node_bytes);
-        kp[i] = ok ? k : kp[i];
-        vp[i] = ok ? v : vp[i];
+        kp[i] = old ? ready(kp[i]) : zero;
+        vp[i] = old ? ready(vp[i]) : zero;
+        kp[i] = fresh ? k : kp[i];
+        vp[i] = fresh ? v : vp[i];
       }
     }
 #pragma unroll
@@ -296,6 +307,13 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
         s[kb] = Mm<T>::mfma(kf, qf[i], s[kb]);
       }
     }
+    // the reads of K four ahead of the products
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < KB * KS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
     const int p0 = tile * KT + wk * KW;
     if (p0 + KW > len) {  // the tile reaches the new nodes or the end
       // Masked as bit operations: with a select on `position < len || bit`, the compiler put the
@@ -317,9 +335,12 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
     top = swap_max(top) * a.scale2;
-    const float mn = fmaxf(m, top);
+    // The base of the weights follows the maximum only where that has left it by LAZY: till then
+    // the weights are above 1, and the sums need no scaling.
+    const bool move = top > m + Mm<T>::LAZY;
+    const float mn = move ? top : m;
     const float base = mn == -__builtin_inff() ? 0.f : mn;  // nothing seen so far: weights 0
-    if (__any(mn > m)) {
+    if (__any(move)) {
       const float f = __builtin_amdgcn_exp2f(m - base);
       l *= f;
 #pragma unroll
@@ -353,33 +374,49 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
           v.y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 8 * VP));
           o[i] = Mm<T>::mfma(__builtin_bit_cast(v8, v), pf[kb][st], o[i]);
         }
+    // a step's weights are worked out under the products of the one before, V read four products ahead
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 28, 0);
+#pragma unroll
+    for (int i = 0; i < KB * 2 * DB; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 28 / DB, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
   };
 
+#pragma unroll
+  for (int i = 0; i < PASS; ++i) {
+    const uint32_t p = (uint32_t)(ch.t0 * KT + lr + i * RPP);
+    Place& x = pl[0][i];
+    x.n = page_of(a.c.div, p, &x.off);
+    x.id = pages[min(x.n, last)];
+  }
   // the barriers for the compiler keep a tile's loads ahead of the products before it
-  ids(ch.t0);
-  load(ch.t0, 0);
   if constexpr (OWN) {
-    ids(ch.t0 + 1);
+    load(ch.t0, 0, pl[0]);
+    ids(pl[0], pl[0]);
     for (int t = ch.t0; t < ch.t1; ++t) {
       store(t, 0, 0);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      load(t + 1, 0);
-      ids(t + 2);
+      load(t + 1, 0, pl[0]);
+      ids(pl[0], pl[0]);
       __builtin_amdgcn_sched_barrier(0);
       compute(t, 0);
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-  } else {
-    ids(ch.t0 + 1);
-    load(ch.t0 + 1, 1);
-    ids(ch.t0 + 2);
+  } else {  // the pages' numbers come before the rows: waiting for them leaves the rows in flight
+    ids(pl[1], pl[0]);
+    load(ch.t0, 0, pl[0]);
+    ids(pl[0], pl[1]);
+    load(ch.t0 + 1, 1, pl[1]);
     store(ch.t0, 0, 0);
     __syncthreads();
-    // tile t of stage h; registers h are free, the others hold tile t + 1
+    // tile t of stage h; registers h are free, the others hold tile t + 1; place h is tile t + 2's
     auto step = [&](int t, int h) {
-      load(t + 2, h);
-      ids(t + 3);
+      ids(pl[h ^ 1], pl[h]);
+      load(t + 2, h, pl[h]);
       __builtin_amdgcn_sched_barrier(0);
       if (wave_live) compute(t, h);
       __builtin_amdgcn_sched_barrier(0);

@@ -64,7 +64,8 @@ pi_status pi_kv_create(pi_ctx* ctx, const pi_kv_desc* desc, pi_kv** out) {
   if (d.head_dim > 256) return fail(ctx, PI_ERR_UNSUPPORTED, "head_dim %d above 256", d.head_dim);
   if (d.page_stride < 0 || d.token_stride < 0 || d.head_stride < 0 || ((d.page_stride | d.token_stride | d.head_stride) & 7))
     return fail(ctx, PI_ERR_INVALID, "cache strides must be multiples of 8 elements");
-  if (d.token_stride >= (1ll << 30)) return fail(ctx, PI_ERR_UNSUPPORTED, "token_stride %lld: below 2^30", (long long)d.token_stride);
+  if (d.page_stride >= (1ll << 35) || d.token_stride >= (1ll << 35))
+    return fail(ctx, PI_ERR_UNSUPPORTED, "page and token strides are below 2^35");
   PI_TRY(check_dev_ptr(ctx, d.k, "k"));
   PI_TRY(check_dev_ptr(ctx, d.v, "v"));
   pi_kv* kv = new (std::nothrow) pi_kv{d, ctx};

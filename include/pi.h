@@ -305,7 +305,7 @@ typedef struct pi_linear pi_linear;
  * h*head_stride.
  *   dtype      PI_T_F16 or PI_T_BF16
  *   heads      key/value heads; head_dim a multiple of 8 up to 256
- *   strides    in elements, multiples of 8; token_stride below 2^30
+ *   strides    in elements, multiples of 8 below 2^35
  * Which pages a sequence has is an argument of the calls: table, int32 [B][table_width] with
  * table_stride elements between sequences, names page table[b][i] for the positions from
  * i*page_tokens on. A NULL table stands for one page each, page b for sequence b. Positions
