@@ -389,7 +389,7 @@ pi_status launch_linear(pi_ctx* c, const LinDev& p) {
   // 4 outputs in one store where every row starts at such a boundary
   const bool wide = p.y_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
   if (p.M <= 16) {
-    PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 2>, dim3((p.N + 31) / 32), 64 * LR_WAVES, 0, p, wide));
+    PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 1>, dim3((p.N + 15) / 16), 64 * LR_WAVES, 0, p, wide));
     return PI_OK;
   }
   const long long big = (long long)((p.N + 255) / 256) * ((p.M + 255) / 256);

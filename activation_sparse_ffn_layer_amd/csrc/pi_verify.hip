@@ -34,7 +34,7 @@ namespace {
 
 constexpr int VF_CH = 4096;        // tokens per chunk
 constexpr int VF_MAX_NODES = 256;
-constexpr int VF_NT = 1024;        // threads of the workgroups that join all rows
+constexpr int VF_NT = 512;         // threads of a workgroup that walks: 8 tokens of a chunk each
 constexpr double VF_NEAR = 2e-5;   // a test with a 32-bit Z decides beyond this distance, relative to p
 
 struct VfPart {   // a chunk of a row, in 32 bits
@@ -254,13 +254,19 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
     if (it == 0.0) next = s.at[cur];
   } else {
     const VfBin* bins = bins_of(p, s.st.stage - DONE, b);
-    VfBin sum{0.0, 0.0, 0.0};
-    for (int k = threadIdx.x; k < p.chunks; k += NT) sum = VfBin{sum.e + bins[k].e, sum.a + bins[k].a, sum.q + bins[k].q};
+    const float un = p.u_next[b];
+    VfBin sum{0.0, 0.0, 0.0};  // of this thread's chunks, the first of which stays in registers
+    if ((int)threadIdx.x < p.chunks) sum = bins[threadIdx.x];
+    const VfBin own = sum;
+    for (int k = threadIdx.x + NT; k < p.chunks; k += NT) sum = VfBin{sum.e + bins[k].e, sum.a + bins[k].a, sum.q + bins[k].q};
     sum = block_sum<NT>(sum, s.red);
     // the chunks' weights: of what is left, or of p where nothing is
     const double iz = 1.0 / sum.e, c = p.q != nullptr ? s.st.c : 0.0;
     const bool left = sum.a * iz - c * sum.q > 0.0;
-    auto weight = [&](int k) { return left ? fmax(bins[k].a * iz - c * bins[k].q, 0.0) : bins[k].e * iz; };
+    auto weight = [&](int k) {
+      const VfBin v = k == (int)threadIdx.x ? own : bins[k];
+      return left ? fmax(v.a * iz - c * v.q, 0.0) : v.e * iz;
+    };
     double total = 0.0;
     for (int k = threadIdx.x; k < p.chunks; k += NT) total += weight(k);
     total = block_sum<NT>(VfBin{total, 0.0, 0.0}, s.red).e;
@@ -289,7 +295,7 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
       return run + incl;
     };
     // the chunk whose running sum passes the target, or the last one with any weight
-    const double target = (double)p.u_next[b] * total;
+    const double target = (double)un * total;
     double carry = 0.0;
     for (int k0 = 0; k0 < p.chunks; k0 += NT) {
       const int k = k0 + (int)threadIdx.x;
@@ -437,21 +443,23 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   constexpr int G = VF_CH / (8 * WAVE * CW);
   const int i0 = chunk * VF_CH + (CW == 1 ? lane : (int)threadIdx.x) * 8;
   constexpr int STEP = 8 * WAVE * CW;
-  float z[G][8];
+  T raw[G][8];  // as stored: half the registers, twice the waves
   float m = -__builtin_inff();
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    if (i0 + g * STEP < p.V) {
-      logits8(row, i0 + g * STEP, p.V, z[g]);
+    const int i = i0 + g * STEP;
+    if (i + 8 <= p.V) {
+      __builtin_memcpy(raw[g], row + i, sizeof raw[g]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[g][j] = -__builtin_inff();
+      for (int j = 0; j < 8; ++j) raw[g][j] = i + j < p.V ? row[min(i + j, p.V - 1)] : (T)-__builtin_inff();
     }
   }
+  auto z = [&](int g, int j) { return clean(to_f32(raw[g][j])); };
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, z[g][j]);
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, z(g, j));
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
   float sum = 0.f;
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[j & 3] += __builtin_amdgcn_exp2f((z[g][j] - m) * it);
+        for (int j = 0; j < 8; ++j) part[j & 3] += __builtin_amdgcn_exp2f((z(g, j) - m) * it);
       sum = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, WAVE);
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
       for (int g = G - 1; g >= 0; --g)
 #pragma unroll
         for (int j = 7; j >= 0; --j)
-          if (z[g][j] == m) at = i0 + g * STEP + j;
+          if (z(g, j) == m) at = i0 + g * STEP + j;
 #pragma unroll
       for (int o = 32; o > 0; o >>= 1) at = min(at, __shfl_xor(at, o, WAVE));
     }
@@ -580,10 +588,10 @@ __device__ __forceinline__ void load_state(const VfDev& p, VfShared& s, int b, i
   __syncthreads();
 }
 
-// Pass `pass`; FIRST: pass 0, which joins the rows' sums. NT threads.
+// Pass `pass`; FIRST: pass 0, which joins the rows' sums.
 template <typename T, bool FIRST>
-__global__ __launch_bounds__(FIRST ? VF_NT : BLOCK) void k_verify_pass(VfDev p, int pass) {
-  constexpr int NT = FIRST ? VF_NT : BLOCK;
+__global__ __launch_bounds__(VF_NT) void k_verify_pass(VfDev p, int pass) {
+  constexpr int NT = VF_NT;
   __shared__ VfShared s;
   const int chunk = blockIdx.x, b = blockIdx.y;
   const bool first = chunk == 0;
@@ -652,7 +660,7 @@ pi_status launch_verify(pi_ctx* c, const VfDev& p) {
   // at 131072 tokens and 5 at 32000. Without a q one is enough but for tests too near to call.
   const int passes = p.q == nullptr ? 1 : std::min(p.chunks > 16 ? 4 : 2, std::max(1, p.N - 1));
   PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, true>, dim3(p.chunks, p.B), VF_NT, 0, p, 0));
-  for (int i = 1; i < passes; ++i) PI_HIP(c, launch_k(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), 0, p, i));
+  for (int i = 1; i < passes; ++i) PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), VF_NT, 0, p, i));
   PI_HIP(c, launch_kb(c, 0, k_verify_end<T>, dim3(p.B), VF_NT, 0, p, passes));
   return PI_OK;
 }
