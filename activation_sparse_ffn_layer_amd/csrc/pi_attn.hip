@@ -88,6 +88,11 @@ template <int KT>
 __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o) {
   const int lane = threadIdx.x % WAVE;
   auto tiles = [&](int b) { return b < a.B ? (kv_len(a.c, a.ctx_len, b) + a.N + KT - 1) / KT : 0; };
+  if (a.B == 1) {
+    const int t = tiles(0), c = (t + a.slots - 1) / a.slots;
+    *o = Chunk{0, slot * c, min(t, slot * c + c), (t + c - 1) / c, 0};
+    return o->t0 < t;
+  }
   const int mine = tiles(lane);  // the sequence of this lane; more than 64 are read again
   auto sum = [&](int c) {
     int n = lane < a.B ? (mine + c - 1) / c : 0;
@@ -682,11 +687,13 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
     return fail(ctx, PI_ERR_OOM, "attention scratch of %zu bytes", ob + mb);
   }
   int32_t* self = reinterpret_cast<int32_t*>(ws + ob + mb);
-  std::vector<int32_t> id(max_batch);
-  for (int i = 0; i < max_batch; ++i) id[i] = i;
-  if (hipMemcpy(self, id.data(), id.size() * 4, hipMemcpyHostToDevice) != hipSuccess) {
-    (void)hipFree(ws);
-    return fail(ctx, PI_ERR_HIP, "filling the attention scratch failed");
+  for (int i0 = 0; i0 < max_batch; i0 += 256) {
+    int32_t id[256];
+    for (int i = 0; i < 256; ++i) id[i] = i0 + i;
+    if (hipMemcpy(self + i0, id, (size_t)std::min(256, max_batch - i0) * 4, hipMemcpyHostToDevice) != hipSuccess) {
+      (void)hipFree(ws);
+      return fail(ctx, PI_ERR_HIP, "filling the attention scratch failed");
+    }
   }
   pi_attn* a = new (std::nothrow) pi_attn{ctx, kv, heads, max_batch, max_nodes, scale, ws, reinterpret_cast<float*>(ws),
                                           reinterpret_cast<float*>(ws + ob), self};

@@ -384,11 +384,16 @@ int split_count(int cus, int tiles, int K) {
   return std::max(1, std::min(2 * cus / tiles, (K + LT_K - 1) / LT_K / 4));
 }
 
+// Up to 16 tokens each workgroup of k_q8_rows reads all of x, which a tile reads once for 128 rows:
+// at K = 8192 and N = 10240 the rows take 20.1 us at one token, 23.1 at 8 and 27.1 at 16, tiles
+// some 20.5; at K = 4096 and N = 12288 11.9, 13.3 and 14.8 against 15.5.
+bool by_rows(int M, int K) { return M == 1 || (M <= 16 && M * K < 65536); }
+
 template <typename T>
 pi_status launch_linear(pi_ctx* c, const LinDev& p) {
   // 4 outputs in one store where every row starts at such a boundary
   const bool wide = p.y_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-  if (p.M <= 16) {
+  if (by_rows(p.M, p.K)) {
     PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 1>, dim3((p.N + 15) / 16), 64 * LR_WAVES, 0, p, wide));
     return PI_OK;
   }
@@ -417,7 +422,7 @@ pi_status pi_linear_create(pi_ctx* ctx, const pi_linear_desc* desc, pi_linear** 
   PI_TRY(check_dev_ptr(ctx, d.w_scale, "w_scale"));
   PI_TRY(check_dev_ptr(ctx, d.bias, "bias", true));
   // one buffer per context: its calls run one after another
-  if (d.max_tokens > 16 && ctx->lin_part == nullptr) {
+  if (d.max_tokens > 1 && ctx->lin_part == nullptr) {
     PI_HIP(ctx, hipSetDevice(ctx->device));
     const size_t bytes = (size_t)2 * ctx->cus * 128 * 128 * 4;
     if (hipMalloc(reinterpret_cast<void**>(&ctx->lin_part), bytes) != hipSuccess) {

@@ -231,11 +231,15 @@ __device__ __forceinline__ VfBin bin_block(const VfDev& p, VfShared& s, int b, d
   return block_sum<NT>(v, s.red);
 }
 
-// The sums of the pass that the walk waited for: Z and the residual's weight.
+// This thread's first chunk of a pass's sums.
+__device__ __forceinline__ VfBin first_bin(const VfDev& p, const VfBin* bins) {
+  return (int)threadIdx.x < p.chunks ? bins[threadIdx.x] : VfBin{0.0, 0.0, 0.0};
+}
+
+// The sums of the pass that the walk waited for: Z and the residual's weight. `v`: first_bin.
 template <int NT>
-__device__ __forceinline__ void join_bins(const VfDev& p, VfShared& s, const VfBin* bins) {
-  VfBin v{0.0, 0.0, 0.0};
-  for (int k = threadIdx.x; k < p.chunks; k += NT) v = VfBin{v.e + bins[k].e, v.a + bins[k].a, v.q + bins[k].q};
+__device__ __forceinline__ void join_bins(const VfDev& p, VfShared& s, const VfBin* bins, VfBin v) {
+  for (int k = threadIdx.x + NT; k < p.chunks; k += NT) v = VfBin{v.e + bins[k].e, v.a + bins[k].a, v.q + bins[k].q};
   v = block_sum<NT>(v, s.red);
   if (threadIdx.x == 0) {
     s.st.z = v.e;
@@ -533,30 +537,42 @@ __device__ __forceinline__ void join_rows(const VfDev& p, VfShared& s, int b, do
       if (p.q != nullptr) qt = p.q[(long long)b * p.qb + (long long)par * p.qn + t];
     }
   }
-  // a wave per row joins its chunks, in a fixed order
-  for (int r = threadIdx.x / WAVE; r < p.N; r += VF_NT / WAVE) {
-    const VfPart* part = p.part + ((long long)b * p.N + r) * p.chunks;
-    float m = -__builtin_inff();
-    VfPart o{m, 0.f, 0x7FFFFFFF, 0};
-    if (lane < p.chunks) o = part[lane];
-    m = o.m;
-    for (int k = lane + WAVE; k < p.chunks; k += WAVE) m = fmaxf(m, part[k].m);
+  // a wave per row joins its chunks, in a fixed order; 4 rows' loads at once
+  constexpr int NW = VF_NT / WAVE, U = 4;
+  const int wave = threadIdx.x / WAVE;
+  const VfPart none{-__builtin_inff(), 0.f, 0x7FFFFFFF, 0};
+  for (int r0 = wave; r0 < p.N; r0 += U * NW) {
+    VfPart o[U];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
-    int at = o.m == m ? o.at : 0x7FFFFFFF;
-    double sum = o.s > 0.f ? (double)o.s * expw(o.m, m, it) : 0.0;
-    for (int k = lane + WAVE; k < p.chunks; k += WAVE) {
-      const VfPart n = part[k];
-      if (n.m == m) at = min(at, n.at);
-      if (n.s > 0.f) sum += (double)n.s * expw(n.m, m, it);
+    for (int n = 0; n < U; ++n) {
+      const int r = r0 + n * NW;
+      o[n] = none;
+      if (r < p.N && lane < p.chunks) o[n] = p.part[((long long)b * p.N + r) * p.chunks + lane];
     }
-    sum = wave_sum_d(sum);
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) at = min(at, __shfl_xor(at, d, WAVE));
-    if (lane == 0) {
-      s.m[r] = m;
-      s.at[r] = at == 0x7FFFFFFF ? -1 : at;
-      s.rs[r] = sum;
+    for (int n = 0; n < U; ++n) {
+      const int r = r0 + n * NW;
+      if (r >= p.N) break;
+      const VfPart* part = p.part + ((long long)b * p.N + r) * p.chunks;
+      float m = o[n].m;
+      for (int k = lane + WAVE; k < p.chunks; k += WAVE) m = fmaxf(m, part[k].m);
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
+      int at = o[n].m == m ? o[n].at : 0x7FFFFFFF;
+      double sum = o[n].s > 0.f ? (double)o[n].s * expw(o[n].m, m, it) : 0.0;
+      for (int k = lane + WAVE; k < p.chunks; k += WAVE) {
+        const VfPart x = part[k];
+        if (x.m == m) at = min(at, x.at);
+        if (x.s > 0.f) sum += (double)x.s * expw(x.m, m, it);
+      }
+      sum = wave_sum_d(sum);
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) at = min(at, __shfl_xor(at, d, WAVE));
+      if (lane == 0) {
+        s.m[r] = m;
+        s.at[r] = at == 0x7FFFFFFF ? -1 : at;
+        s.rs[r] = sum;
+      }
     }
   }
   __syncthreads();
@@ -601,17 +617,17 @@ __global__ __launch_bounds__(VF_NT) void k_verify_pass(VfDev p, int pass) {
     join_rows<T>(p, s, b, it, first);
     walk(p, s, b, it, 0, first);
   } else {
-    const VfState* was = p.state + (long long)(pass & 1) * p.B + b;
     const int src = (pass - 1) & 1;
-    if (was->stage != WAIT_REST) {
+    const VfBin v = first_bin(p, bins_of(p, src, b));  // all loads before the first is waited for
+    load_state(p, s, b, pass);
+    if (s.st.stage != WAIT_REST) {
       if (first && threadIdx.x == 0) {
-        *now = *was;
-        if (was->stage == WAIT_DRAW) now->stage = DONE + src;
+        *now = s.st;
+        if (s.st.stage == WAIT_DRAW) now->stage = DONE + src;
       }
       return;
     }
-    load_state(p, s, b, pass);
-    join_bins<NT>(p, s, bins_of(p, src, b));
+    join_bins<NT>(p, s, bins_of(p, src, b), v);
     walk(p, s, b, it, src, first);
   }
   if (first && threadIdx.x == 0) *now = s.st;
@@ -635,7 +651,7 @@ __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
       __syncthreads();
       break;
     }
-    join_bins<VF_NT>(p, s, bins_of(p, src, b));
+    join_bins<VF_NT>(p, s, bins_of(p, src, b), first_bin(p, bins_of(p, src, b)));
     walk(p, s, b, it, src, true);
     if (s.st.stage >= DONE) break;
     src = 2;
