@@ -75,7 +75,35 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(NormDev p) {
     for (int i = 0; i < 8; ++i) ss += h[j][i] * h[j][i];
   }
   ss = block_fold<NW, false>(ss, red[0]);
-  const float rinv = 1.0f / sqrtf(ss / (float)p.d + p.eps);
+  const float mean = ss / (float)p.d + p.eps;
+  float rinv = mean > 0.f ? 1.0f / sqrtf(mean) : 0.f;  // a row of zeros, without eps: zeros
+  bool bad = !(ss < __builtin_inff());
+  if (bad || mean < 1e-30f) {
+    // Squares beyond fp32's range, or lost below it: again with the row's largest element near 1. A
+    // NaN makes the sum one; an infinity is its row's largest.
+    float big = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(h[j][i]));
+    big = block_fold<NW, true>(big, red[1]);
+    bad = ss != ss || !(big < __builtin_inff());
+    if (!bad && big > 0.f) {
+      const int e = -ilogbf(big);
+      float s2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = ldexpf(h[j][i], e);
+          s2 += x * x;
+        }
+      __syncthreads();  // red is free again
+      s2 = block_fold<NW, false>(s2, red[0]);
+      rinv = ldexpf(1.0f / sqrtf(s2 / (float)p.d + ldexpf(ldexpf(p.eps, e), e)), e);
+    }
+    __syncthreads();
+  }
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -98,7 +126,6 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(NormDev p) {
   if (p.q == nullptr) return;
   top = block_fold<NW, true>(top, red[1]);
   // a row with an infinity or a NaN has no scale: NaN, and zeros beside it
-  const bool bad = !(ss < __builtin_inff());
   const float scale = top / 127.0f;
   const float inv = (scale > 0.f && !bad) ? 1.0f / scale : 0.f;
   if (threadIdx.x == 0) p.scale[row] = bad ? __builtin_nanf("") : scale;

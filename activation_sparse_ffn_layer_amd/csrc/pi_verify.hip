@@ -131,10 +131,29 @@ __device__ __forceinline__ double pow2(double t) {
 // exp((z - m) / T), given it = log2(e) / T; z <= m, m finite
 __device__ __forceinline__ double expw(float z, float m, double it) { return pow2(((double)z - (double)m) * it); }
 
-__device__ __forceinline__ double wave_sum_d(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, WAVE);
+// v of the lane that a data-parallel move brings it from, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Inclusive running sum over the wave's lanes: within rows of 16 by shifts of 1, 2, 4 and 8, then the
+// sums of the rows before (row_bcast 15 and 31). A quarter of the latency of lane permutes.
+__device__ __forceinline__ double wave_scan_d(double v) {
+  v += moved<0x111, 0xF>(v);
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);
+  v += moved<0x143, 0xC>(v);
   return v;
+}
+__device__ __forceinline__ double wave_sum_d(double v) {  // the same on every lane
+  const uint64_t b = __builtin_bit_cast(uint64_t, wave_scan_d(v));
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, WAVE - 1), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), WAVE - 1);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // Sums over the workgroup's NT threads, the same on every thread; red: 3 NT / WAVE doubles.
@@ -253,6 +272,9 @@ template <typename T>
 __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, double it) {
   constexpr int NT = VF_NT;
   const int cur = s.st.cur, lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int depth = s.st.depth;  // nodes of the path; its nodes are written already
+  static_assert(VF_MAX_NODES <= NT, "a thread per node");
+  const int i1 = threadIdx.x + 1, node1 = i1 < depth ? p.nodes[(long long)b * p.N + i1] : -1;
   int next = -1;
   if (s.st.stage == DONE_PLAIN) {
     if (it == 0.0) next = s.at[cur];
@@ -271,23 +293,14 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
       const VfBin v = k == (int)threadIdx.x ? own : bins[k];
       return left ? fmax(v.a * iz - c * v.q, 0.0) : v.e * iz;
     };
-    double total = 0.0;
-    for (int k = threadIdx.x; k < p.chunks; k += NT) total += weight(k);
-    total = block_sum<NT>(VfBin{total, 0.0, 0.0}, s.red).e;
     if (threadIdx.x == 0) {
       s.before = 0.0;
       s.pick = 0x7FFFFFFF;
       s.last = -1;
     }
-    __syncthreads();
     // inclusive sum over the workgroup of one value per thread, from `carry` on
     auto scan = [&](double v, double* carry) {
-      double incl = v;
-#pragma unroll
-      for (int o = 1; o < WAVE; o <<= 1) {
-        const double t = __shfl_up(incl, o, WAVE);
-        if (lane >= o) incl += t;
-      }
+      const double incl = wave_scan_d(v);
       __syncthreads();
       if (lane == WAVE - 1) s.red[wave].e = incl;
       __syncthreads();
@@ -299,12 +312,19 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
       return run + incl;
     };
     // the chunk whose running sum passes the target, or the last one with any weight
+    const double v0 = (int)threadIdx.x < p.chunks ? weight(threadIdx.x) : 0.0;
+    double total = 0.0;
+    const double run0 = scan(v0, &total);
+    for (int k0 = NT; k0 < p.chunks; k0 += NT) {
+      const int k = k0 + (int)threadIdx.x;
+      scan(k < p.chunks ? weight(k) : 0.0, &total);
+    }
     const double target = (double)un * total;
     double carry = 0.0;
     for (int k0 = 0; k0 < p.chunks; k0 += NT) {
       const int k = k0 + (int)threadIdx.x;
-      const double v = k < p.chunks ? weight(k) : 0.0;
-      const double run = scan(v, &carry);
+      const double v = k0 == 0 ? v0 : k < p.chunks ? weight(k) : 0.0;
+      const double run = k0 == 0 && p.chunks <= NT ? run0 : scan(v, &carry);
       if (v > 0.0 && run > target) atomicMin(&s.pick, k);
       if (v > 0.0) atomicMax(&s.last, k);
       __syncthreads();
@@ -338,8 +358,8 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
         all += w[j];
         if (w[j] > 0.0) lastw = i + j;
       }
-      carry = 0.0;
-      double run = scan(all, &carry) - all;
+      double none = 0.0;
+      double run = scan(all, &none) - all;
       int mine = 0x7FFFFFFF;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -352,12 +372,9 @@ __device__ __forceinline__ void finish(const VfDev& p, VfShared& s, int b, doubl
       next = s.pick != 0x7FFFFFFF ? s.pick : s.last;
     }
   }
-  const int depth = s.st.depth;  // nodes of the path; its nodes are written already
-  for (int k = threadIdx.x; k < p.N; k += NT) {
-    int o = -1;
-    if (k + 1 < depth) o = s.tok[p.nodes[(long long)b * p.N + k + 1]];
-    else if (k + 1 == depth) o = next;
-    p.out[(long long)b * p.N + k] = o;
+  const int k = threadIdx.x;
+  if (k < p.N) {
+    p.out[(long long)b * p.N + k] = node1 >= 0 ? s.tok[node1] : k + 1 == depth ? next : -1;
     if (k >= depth) p.nodes[(long long)b * p.N + k] = -1;
   }
   if (threadIdx.x == 0) p.n[b] = depth;
