@@ -24,8 +24,8 @@ def _bad(msg: str):
     raise PiError(PI_ERR_INVALID, msg)
 
 
-def _need(t, name: str, dtype, shape, device: int) -> int:
-    """Device pointer of a tensor of this type and shape (dense up to its strides)."""
+def _refuse(t, name: str, dtype, shape, device: int):
+    """Say what is wrong with a tensor that did not pass."""
     if not isinstance(t, torch.Tensor):
         _bad(f"{name} is no tensor")
     if t.dtype is not dtype:
@@ -34,14 +34,17 @@ def _need(t, name: str, dtype, shape, device: int) -> int:
         _bad(f"{name} has shape {tuple(t.shape)}, need {tuple(shape)}")
     if t.get_device() != device:
         _bad(f"{name} is on {t.device}, need GPU {device}")
-    return t.data_ptr()
+    _bad(f"{name} must be contiguous")
 
+
+# The calls are short next to their checks' cost on the host: the checks that pass are one expression.
 
 def _dense(t, name: str, dtype, shape, device: int) -> int:
-    p = _need(t, name, dtype, shape, device)
-    if not t.is_contiguous():
-        _bad(f"{name} must be contiguous")
-    return p
+    """Device pointer of a contiguous tensor of this type and shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
 
 
 def _opt(t, name: str, dtype, shape, device: int) -> Optional[int]:
@@ -50,11 +53,12 @@ def _opt(t, name: str, dtype, shape, device: int) -> Optional[int]:
 
 def _view(t, name: str, dtype, shape, device: int):
     """Device pointer and strides of a tensor whose last axis is contiguous."""
-    p = _need(t, name, dtype, shape, device)
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] != 1:
-        _bad(f"{name}: the last axis must be contiguous")
-    return p, s
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        s = t.stride()
+        if s[-1] != 1 and shape[-1] != 1:
+            _bad(f"{name}: the last axis must be contiguous")
+        return t.data_ptr(), s
+    _refuse(t, name, dtype, shape, device)
 
 
 def _borrow(ctx, *tensors):

@@ -14,7 +14,6 @@ MI355X's 8 TB/s), and the fp64 CPU oracle timed on a bounded sample of the same 
 """
 import argparse
 import dataclasses
-import glob
 import hashlib
 import json
 import math
@@ -61,11 +60,15 @@ def parse():
     return ap.parse_args()
 
 
+# what the stack's kernels and launches are built from
+STACK_SOURCES = ("pi_device.hpp", "pi_kernels.hpp", "pi_lib.hip", "pi_mfma.hpp")
+
+
 def kernel_source_hash():
-    """Hash of the HIP sources; a recorded counter reading is used only while it matches."""
+    """Hash of the stack's HIP sources; a recorded counter reading is used only while it matches."""
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "activation_sparse_ffn_layer_amd", "csrc", "*"))):
-        with open(f, "rb") as fh:
+    for f in STACK_SOURCES:
+        with open(os.path.join(ROOT, "activation_sparse_ffn_layer_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:12]
 
