@@ -12,6 +12,15 @@
 // The keys of a sequence are one axis: its cached positions, then its N new nodes. The axis is
 // cut in chunks of whole tiles, equally long for all sequences, so that the chunks of all heads
 // fill the chip once; partial results (O, max, sum) are joined by k_attn_join.
+//
+// Many rows are bound by the products and the weights' exponentials, which take the SIMDs nearly in
+// turn (47% and 48% of the busy cycles) at a clock that falls to 1.75 GHz: 64 nodes of 64 heads (8
+// key heads) over 65536 positions of 128, 137 GFLOP, 155 to 185 us and 10 us for the join. 26 nodes
+// of 4 sequences (25 000 positions, 108 MB): 41 us and 10 us. One node of 32 heads over 512
+// positions is a chain of latencies: 10 us and 4 us; joining in the last workgroup to arrive
+// instead took 22 us (its release fences). Four waves of 32 rows (two workgroups per CU) were
+// slower than eight, 62 against 54 us and 227 against 190; so was working a block's scores out
+// under the weights of the one before, 60 and 211.
 #include <algorithm>
 #include <new>
 
@@ -536,6 +545,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   }
 }
 
+// Bound by memory, the partial results' bytes (27 MB at 6656 rows in some 13 chunks: 10 us).
 // out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over a sequence's chunks s, one wave per
 // query row, 4 columns per lane; rows of sequences of one chunk are done already.
 template <typename T, int DP, int KT>

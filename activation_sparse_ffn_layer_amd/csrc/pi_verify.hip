@@ -12,7 +12,8 @@
 // whose test is nearer than that waits for its row's Z in 64 bits.
 //
 //   k_verify_rows   every row's maximum and 32-bit sum, in chunks of the vocabulary: the one pass
-//                   over all logits, bound by memory
+//                   over all logits, bound by memory. 512 rows of 131072 fp16 logits, 134 MB:
+//                   29 us, 4.6 TB/s (72 us with all exponentials in 64 bits)
 //   k_verify_pass   walks the tree as far as it can, then sums in 64 bits, in the same chunks, what
 //                   the walk waits for: over the current row the exponentials (E), those of
 //                   the tokens with p > c q (A) and these tokens' q (Q). Then Z = E and
@@ -22,6 +23,8 @@
 //                   once where the sequence is done).
 //   k_verify_end    a workgroup per sequence does whatever is left and draws the next token: the
 //                   chunk by the chunks' weights, then the token inside it.
+// The passes and the end are chains of dependent loads, sums over a workgroup and the walk: 15, 7
+// and 12 us at 16 trees of 32 nodes, 8, 3 and 10 at one chain of 5.
 #include <algorithm>
 #include <new>
 
