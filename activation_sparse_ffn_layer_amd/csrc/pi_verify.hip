@@ -159,6 +159,28 @@ __device__ __forceinline__ double wave_sum_d(double v) {  // the same on every l
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// The same for floats: sum and maximum over the wave, the same on every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v, float none) {
+  return u2f(__builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+}
+template <typename F>
+__device__ __forceinline__ float wave_fold(float v, float none, F f) {
+  v = f(v, moved<0x111, 0xF>(v, none));
+  v = f(v, moved<0x112, 0xF>(v, none));
+  v = f(v, moved<0x114, 0xF>(v, none));
+  v = f(v, moved<0x118, 0xF>(v, none));
+  v = f(v, moved<0x142, 0xA>(v, none));
+  v = f(v, moved<0x143, 0xC>(v, none));
+  return u2f((uint32_t)__builtin_amdgcn_readlane(__builtin_bit_cast(int, v), WAVE - 1));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_fold(v, -__builtin_inff(), [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_fold(v, 0.f, [](float a, float b) { return a + b; });
+}
+
 // Sums over the workgroup's NT threads, the same on every thread; red: 3 NT / WAVE doubles.
 template <int NT>
 __device__ __forceinline__ VfBin block_sum(VfBin v, VfBin* red) {
@@ -251,6 +273,15 @@ __device__ __forceinline__ VfBin bin_block(const VfDev& p, VfShared& s, int b, d
   for (int g = 0; g < VF_CH / 8; g += NT)
     if (NT <= VF_CH / 8 || threadIdx.x < VF_CH / 8) bin8<T>(p, s, b, it, chunk * VF_CH + (g + (int)threadIdx.x) * 8, &v);
   return block_sum<NT>(v, s.red);
+}
+
+// The same by one wave.
+template <typename T>
+__device__ __forceinline__ VfBin bin_wave(const VfDev& p, const VfShared& s, int b, double it, int chunk) {
+  VfBin v{0.0, 0.0, 0.0};
+#pragma unroll 2
+  for (int g = 0; g < VF_CH / 8; g += WAVE) bin8<T>(p, s, b, it, chunk * VF_CH + (g + (int)threadIdx.x % WAVE) * 8, &v);
+  return VfBin{wave_sum_d(v.e), wave_sum_d(v.a), wave_sum_d(v.q)};
 }
 
 // This thread's first chunk of a pass's sums.
@@ -484,8 +515,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, z(g, j));
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
+  m = wave_max(m);
   float sum = 0.f;
   int at = 0x7FFFFFFF;
   if (m > -__builtin_inff()) {
@@ -495,9 +525,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int j = 0; j < 8; ++j) part[j & 3] += __builtin_amdgcn_exp2f((z(g, j) - m) * it);
-      sum = (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, WAVE);
+      sum = wave_sum((part[0] + part[1]) + (part[2] + part[3]));
     } else {
 #pragma unroll
       for (int g = G - 1; g >= 0; --g)
@@ -576,8 +604,7 @@ __device__ __forceinline__ void join_rows(const VfDev& p, VfShared& s, int b, do
       const VfPart* part = p.part + ((long long)b * p.N + r) * p.chunks;
       float m = o[n].m;
       for (int k = lane + WAVE; k < p.chunks; k += WAVE) m = fmaxf(m, part[k].m);
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, WAVE));
+      m = wave_max(m);
       int at = o[n].m == m ? o[n].at : 0x7FFFFFFF;
       double sum = o[n].s > 0.f ? (double)o[n].s * expw(o[n].m, m, it) : 0.0;
       for (int k = lane + WAVE; k < p.chunks; k += WAVE) {
@@ -586,8 +613,10 @@ __device__ __forceinline__ void join_rows(const VfDev& p, VfShared& s, int b, do
         if (x.s > 0.f) sum += (double)x.s * expw(x.m, m, it);
       }
       sum = wave_sum_d(sum);
+      if (it == 0.0) {  // greedy rows only have it
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) at = min(at, __shfl_xor(at, d, WAVE));
+        for (int d = 32; d > 0; d >>= 1) at = min(at, __shfl_xor(at, d, WAVE));
+      }
       if (lane == 0) {
         s.m[r] = m;
         s.at[r] = at == 0x7FFFFFFF ? -1 : at;
@@ -675,9 +704,9 @@ __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
     walk(p, s, b, it, src, true);
     if (s.st.stage >= DONE) break;
     src = 2;
-    for (int k = 0; k < p.chunks; ++k) {
-      const VfBin v = bin_block<T, VF_NT>(p, s, b, it, k);
-      if (threadIdx.x == 0) bins_of(p, 2, b)[k] = v;
+    for (int k = threadIdx.x / WAVE; k < p.chunks; k += VF_NT / WAVE) {
+      const VfBin v = bin_wave<T>(p, s, b, it, k);
+      if (threadIdx.x % WAVE == 0) bins_of(p, 2, b)[k] = v;
     }
     __threadfence_block();
     __syncthreads();
@@ -692,9 +721,12 @@ pi_status launch_verify(pi_ctx* c, const VfDev& p) {
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, 1>, dim3((p.chunks + NWAVES - 1) / NWAVES, p.N, p.B), 0, p));
   else
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, NWAVES>, dim3(p.chunks, p.N, p.B), 0, p));
-  // A pass that finds nothing to do costs 2 us; one that the last kernel does by itself some 20 us
-  // at 131072 tokens and 5 at 32000. Without a q one is enough but for tests too near to call.
-  const int passes = p.q == nullptr ? 1 : std::min(p.chunks > 16 ? 4 : 2, std::max(1, p.N - 1));
+  // A pass costs 2.7 us where it finds nothing to do and some 7 where it does; what is left after them
+  // the last kernel does at 63 us a residual of 131072 tokens and 17 of 32000, on one CU. A path
+  // has few rejections, more in trees of more nodes. Without a q one pass is enough but for
+  // tests too near to call.
+  const int most = p.chunks > 16 ? 6 : p.N > 8 ? 4 : 2;
+  const int passes = p.q == nullptr ? 1 : std::min(most, std::max(1, p.N - 1));
   PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, true>, dim3(p.chunks, p.B), VF_NT, 0, p, 0));
   for (int i = 1; i < passes; ++i) PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), VF_NT, 0, p, i));
   PI_HIP(c, launch_kb(c, 0, k_verify_end<T>, dim3(p.B), VF_NT, 0, p, passes));
