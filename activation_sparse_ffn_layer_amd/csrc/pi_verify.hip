@@ -723,9 +723,10 @@ pi_status launch_verify(pi_ctx* c, const VfDev& p) {
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, NWAVES>, dim3(p.chunks, p.N, p.B), 0, p));
   // A pass costs 2.7 us where it finds nothing to do and some 7 where it does; what is left after them
   // the last kernel does at 63 us a residual of 131072 tokens and 17 of 32000, on one CU. A path
-  // has few rejections, more in trees of more nodes. Without a q one pass is enough but for
-  // tests too near to call.
-  const int most = p.chunks > 16 ? 6 : p.N > 8 ? 4 : 2;
+  // has few rejections; trees of more nodes and batches of more sequences are likelier to have
+  // one with many (16 trees of 32 nodes: 82 to 87 us with 4 passes, 88 to 92 with 6, none left
+  // over in either). Without a q one pass is enough but for tests too near to call.
+  const int most = p.chunks > 16 ? (p.B > 16 ? 6 : 4) : p.N > 8 ? 4 : 2;
   const int passes = p.q == nullptr ? 1 : std::min(most, std::max(1, p.N - 1));
   PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, true>, dim3(p.chunks, p.B), VF_NT, 0, p, 0));
   for (int i = 1; i < passes; ++i) PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), VF_NT, 0, p, i));
