@@ -190,6 +190,13 @@ def test_verify_rejections_of_large_vocabularies(ctx, V, N, u):
     base.check_verify(base.run_verify(ctx, dict(c, q=None)), dict(c, q=None))
 
 
+def test_verify_many_sequences_of_a_large_vocabulary(ctx):
+    """A batch that takes the longer run of passes, its sequences done after unlike numbers of them."""
+    c = base.verify_case(17, 9, 66001, F16, 3, True, 1.0, 5)
+    c["u"] = (c["u"] * torch.linspace(0.2, 1.0, 17)[:, None] + 0.3).clamp(max=0.999)
+    base.check_verify(base.run_verify(ctx, c), c)
+
+
 def test_verify_very_cold_and_very_hot(ctx):
     for temp in (1e-3, 1e-30, 1e6):
         c = base.verify_case(2, 5, 3000, F32, 2, False, 1.0, 3)
