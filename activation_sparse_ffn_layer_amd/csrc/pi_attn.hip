@@ -596,7 +596,8 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = s + HALVES * u + mine;
-        v += x[u] * __shfl(c < n ? f : 0.f, min(c, n - 1), WAVE) * (c < n ? 1.f : 0.f);
+        // the halves ask different lanes: what is shuffled must not depend on the asking lane's c
+        v += x[u] * __shfl(f, min(c, n - 1), WAVE) * (c < n ? 1.f : 0.f);
       }
     }
   }
