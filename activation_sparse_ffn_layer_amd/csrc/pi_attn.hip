@@ -154,13 +154,25 @@ constexpr size_t attn_lds() {
   return tile > merge ? tile : merge;
 }
 
+// Lanes that load one row, a power of two, and the 16-byte piece that a lane loads: where a row has
+// fewer pieces than lanes (heads of 96), the lanes past them load the last one again.
+constexpr int row_lanes(int DP) { return DP <= 64 ? 8 : DP <= 128 ? 16 : 32; }
+constexpr int row_piece(int DP, int lane) { return lane < DP / 8 ? lane : DP / 8 - 1; }
+constexpr bool loads_stay_in_row(int DP) {
+  for (int lane = 0; lane < row_lanes(DP); ++lane)
+    if (16 * row_piece(DP, lane) + 16 > 2 * DP) return false;
+  return row_lanes(DP) * 8 >= DP;
+}
+static_assert(loads_stay_in_row(64) && loads_stay_in_row(96) && loads_stay_in_row(128) && loads_stay_in_row(256),
+              "a tile's loads end with the row, which may be the cache's last");
+
 // WQ waves along the query rows (32 each), WK along a tile's keys (32 KB each). With WQ == 1 a
 // wave loads and reads its own keys only and the tile loop has no barrier.
 template <typename T, int DP, int WQ, int WK, int KB>
 __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tree_attn(AttnDev a) {
   constexpr int KW = 32 * KB, KT = KW * WK, NT = 64 * WQ * WK;
   constexpr bool OWN = WQ == 1;                          // tiles private to a wave
-  constexpr int LPR = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // lanes that load one row
+  constexpr int LPR = row_lanes(DP);
   constexpr int LROWS = OWN ? KW : KT, LTHR = OWN ? 64 : NT;
   constexpr int RPP = LTHR / LPR, PASS = LROWS / RPP;
   static_assert(PASS >= 1 && LROWS % RPP == 0, "a tile is whole passes");
@@ -200,6 +212,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   // loading: pass i of a thread is row lr + i * RPP of the tile (of the wave's part), piece lc
   const int lt = OWN ? lane : (int)threadIdx.x;
   const int lr = lt / LPR + (OWN ? wk * KW : 0), lc = lt % LPR;
+  const int le = 8 * row_piece(DP, lc);
   const bool piece_in = lc * 8 < a.D;
   uint8_t* const ks = smem + (OWN ? wk * KW * (KP + VP) : 0);
   const long long nhead = (long long)hk * a.kv_head + (long long)b * a.kv_batch;
@@ -212,9 +225,9 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   // global pointers by type: a generic load counts as a read of LDS too, and holds those up
   typedef const __attribute__((address_space(1))) uint8_t* gp;
   const gp zero = (gp)(const uint8_t*)&attn_zero;
-  const gp kc = (gp)(static_cast<const uint8_t*>(a.c.k) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
-  const gp vc = (gp)(static_cast<const uint8_t*>(a.c.v) + 2 * ((long long)hk * a.c.head_stride + lc * 8));
-  const gp kn = (gp)(a.kn + 2 * (nhead + lc * 8)), vn = (gp)(a.vn + 2 * (nhead + lc * 8));
+  const gp kc = (gp)(static_cast<const uint8_t*>(a.c.k) + 2 * ((long long)hk * a.c.head_stride + le));
+  const gp vc = (gp)(static_cast<const uint8_t*>(a.c.v) + 2 * ((long long)hk * a.c.head_stride + le));
+  const gp kn = (gp)(a.kn + 2 * (nhead + le)), vn = (gp)(a.vn + 2 * (nhead + le));
   const uint32_t page_units = (uint32_t)(a.c.page_stride >> 3), token_units = (uint32_t)(a.c.token_stride >> 3);  // 16 bytes
   const long long node_bytes = 2 * a.kv_node;
   const uint32_t npages = (uint32_t)a.c.pages;
