@@ -610,7 +610,14 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
       for (int u = 0; u < U; ++u) {
         const int c = s + HALVES * u + mine;
         // the halves ask different lanes: what is shuffled must not depend on the asking lane's c
-        v += x[u] * __shfl(f, min(c, n - 1), WAVE) * (c < n ? 1.f : 0.f);
+        const float g = __shfl(f, min(c, n - 1), WAVE);
+        // Selected, not multiplied by zero: a part may hold an infinity that the row sees, which stays one
+        // whatever its chunk weighs.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = fabsf(x[u][i]) == __builtin_inff() ? x[u][i] : x[u][i] * g;
+          v[i] += c < n ? y : 0.f;
+        }
       }
     }
   }

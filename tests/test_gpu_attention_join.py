@@ -63,3 +63,28 @@ def test_long_decode_of_a_grouped_head_model(ctx):
     kn = (q.view(1, 1, HK, H // HK, D).float().mean(3)).to(BF16)  # the newest token answers its queries
     out = base.run_attention(ctx, q, k, v, kn, vn, None, table, [n], D ** -0.5)
     base.check_attention(out, q, k, v, kn, vn, base.sees_of([[-1]]), table, [n], D ** -0.5)
+
+
+@pytest.mark.parametrize("score", [0.0, -200.0])
+@pytest.mark.parametrize("n", [20, 700, 768, 4400])
+@pytest.mark.parametrize("HK,D,dtype", [(1, 64, F16), (8, 128, BF16), (2, 256, F16)])
+def test_infinities_that_a_node_sees(ctx, HK, D, dtype, n, score):
+    """One chunk or many, a number of them that is no multiple of 8, and a last one that weighs nothing
+    beside the others: an infinite value is the output of the node that sees it, and of no other."""
+    N = 3
+    g = torch.Generator().manual_seed(n)
+    k, v, table = base.make_cache(ctx, [n], n + N, HK, D, 16, dtype, 4)
+    k.zero_()
+    q = torch.ones(1, N, HK, D, dtype=dtype)
+    kn = torch.full((1, N, HK, D), score / D, dtype=dtype)
+    vn = torch.randn(1, N, HK, D, generator=g).to(dtype)
+    clean = vn.clone()
+    vn[0, 1, :, 5], vn[0, 1, :, 6], vn[0, 1, :, 7] = float("inf"), float("-inf"), float("nan")
+    clean[0, 1, :, 5:8] = 0
+    sees = torch.eye(N, dtype=torch.bool)[None]
+    out = base.run_attention(ctx, q, k, v, kn, vn, base.words_of(sees), table, [n], 1.0).cpu()
+    assert (out[0, 1, :, 5] == float("inf")).all() and (out[0, 1, :, 6] == float("-inf")).all()
+    assert out[0, 1, :, 7].isnan().all()
+    want = base.ref.tree_attention(q, k, v, kn, clean, sees, table, [n], 1.0)[0]
+    out[0, 1, :, 5:8] = want[0, 1, :, 5:8].to(dtype)
+    base.check_attention(out, q, k, v, kn, clean, sees, table, [n], 1.0)
