@@ -86,6 +86,20 @@ __device__ __forceinline__ float swap_add(float v) {
   return u2f(p[0]) + u2f(p[1]);
 }
 
+// Tiles of KT keys that a sequence's positions and nodes take. Positions go up to 2^31 - 65 and a tile
+// or its successors may end beyond 2^31: sums of them are unsigned, and the kernels go by a tile's
+// place relative to the sequence's end, which is small where it matters.
+template <int KT>
+__device__ __forceinline__ int key_tiles(const AttnDev& a, int b) {
+  return (int)(((uint32_t)kv_len(a.c, a.ctx_len, b) + (uint32_t)(a.N + KT - 1)) / (uint32_t)KT);
+}
+template <int KT>
+__device__ __forceinline__ int tile_from_end(int tile, int len) {
+  return (int)((uint32_t)tile * (uint32_t)KT - (uint32_t)len);
+}
+// Sums of tiles over sequences stop at 2^30, far above the slots that they are compared with.
+__device__ __forceinline__ uint32_t add_tiles(uint32_t a, uint32_t b) { return min(a + b, 1u << 30); }
+
 // Where chunk `slot` lies: sequence b, its tiles [t0, t1), its number of chunks and the first
 // one's slot; false past the last chunk. Chunks are `c` tiles long, the least c that needs no
 // more than `slots` of them in all (slots >= B). Every wave works it out for itself.
@@ -95,7 +109,7 @@ struct Chunk {
 template <int KT>
 __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o) {
   const int lane = threadIdx.x % WAVE;
-  auto tiles = [&](int b) { return b < a.B ? (kv_len(a.c, a.ctx_len, b) + a.N + KT - 1) / KT : 0; };
+  auto tiles = [&](int b) { return b < a.B ? key_tiles<KT>(a, b) : 0; };
   if (a.B == 1) {
     const int t = tiles(0), c = (t + a.slots - 1) / a.slots;
     *o = Chunk{0, slot * c, min(t, slot * c + c), (t + c - 1) / c, 0};
@@ -103,11 +117,11 @@ __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o)
   }
   const int mine = tiles(lane);  // the sequence of this lane; more than 64 are read again
   auto sum = [&](int c) {
-    int n = lane < a.B ? (mine + c - 1) / c : 0;
-    for (int b = lane + WAVE; b < a.B; b += WAVE) n += (tiles(b) + c - 1) / c;
+    uint32_t n = lane < a.B ? (mine + c - 1) / c : 0;
+    for (int b = lane + WAVE; b < a.B; b += WAVE) n = add_tiles(n, (tiles(b) + c - 1) / c);
 #pragma unroll
-    for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
-    return n;
+    for (int s = 32; s > 0; s >>= 1) n = add_tiles(n, __shfl_xor(n, s, WAVE));
+    return (int)n;
   };
   const int total = sum(1);
   int c = max(1, (total + a.slots - 1) / a.slots);
@@ -264,12 +278,12 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
       vp[i] = vc + (at << 4);
       bad |= (uint32_t)p[i].id >= npages;
     }
-    if (tile * KT + KT > len || a.D != DP || __any(bad)) {  // not all rows are whole rows of the cache
-      const int p0 = tile * KT + lr;
+    const int end = tile_from_end<KT>(tile, len);
+    if (end + KT > 0 || a.D != DP || __any(bad)) {  // not all rows are whole rows of the cache
       const bool in = piece_in & (tile < ch.t1);
 #pragma unroll
       for (int i = 0; i < PASS; ++i) {
-        const int j = p0 + i * RPP - len;
+        const int j = end + lr + i * RPP;
         const bool old = in & (j < 0) & ((uint32_t)p[i].id < npages), fresh = in & (j >= 0) & (j < a.N);
         const gp k = ready(kn + j * node_bytes), v = ready(vn + j * node_bytes);
         kp[i] = old ? ready(kp[i]) : zero;
@@ -288,13 +302,14 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int STAGE = LROWS * (KP + VP);
   auto store = [&](int tile, int stage, int set) {
     uint8_t* base = ks + stage * STAGE;
-    if (tile * KT + KT > len) {
+    const int end = tile_from_end<KT>(tile, len);
+    if (end + KT > 0) {
       // A weight of zero times an infinity or a NaN is a NaN: such elements of the new nodes, whom
       // not every row sees, stay out of the product and are added to the rows that see them at
       // the end (every row sees the cached positions, where nothing has to be done).
 #pragma unroll
       for (int i = 0; i < PASS; ++i)
-        if (tile * KT + lr + i * RPP >= len) {
+        if (end + lr + i * RPP >= 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t w = vr[set][i][e];
@@ -343,13 +358,13 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
-    const int p0 = tile * KT + wk * KW;
-    if (p0 + KW > len) {  // the tile reaches the new nodes or the end
+    const int end = tile_from_end<KT>(tile, len) + wk * KW;
+    if (end + KW > 0) {  // the tile reaches the new nodes or the end
       // Masked as bit operations: with a select on `position < len || bit`, the compiler put the
       // -inf of the untaken side over the accumulators of lanes that keep theirs.
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const int j0 = p0 + kb * 32 - len;  // the node of the block's first key
+        const int j0 = end + kb * 32;  // the node of the block's first key
         uint32_t vis = j0 >= 64 ? 0u : (uint32_t)(seen >> (j0 & 63));
         if (j0 < 0) vis = j0 <= -32 ? ~0u : (uint32_t)(seen << -j0) | ((1u << -j0) - 1);
         vis >>= 4 * half;
@@ -416,7 +431,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
 
 #pragma unroll
   for (int i = 0; i < PASS; ++i) {
-    const uint32_t p = (uint32_t)(ch.t0 * KT + lr + i * RPP);
+    const uint32_t p = (uint32_t)ch.t0 * KT + (uint32_t)(lr + i * RPP);
     Place& x = pl[0][i];
     x.n = page_of(a.c.div, p, &x.off);
     x.id = pages[min(x.n, last)];
@@ -467,7 +482,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
     const int rn = r / a.G;
     const uint64_t w = a.tree != nullptr ? a.tree[(long long)b * a.N + rn] : (2ull << rn) - 1;
     for (int j = 0; j < a.N; ++j)
-      if (((w >> j) & 1) && len + j >= ch.t0 * KT && len + j < ch.t1 * KT) {
+      if (((w >> j) & 1) && j >= tile_from_end<KT>(ch.t0, len) && j < tile_from_end<KT>(ch.t1, len)) {
         const T* x = reinterpret_cast<const T*>(a.vn) + nhead + (long long)j * a.kv_node + d;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -569,13 +584,13 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
   if (id >= rows) return;
   const int r = id % a.R, hk = id / a.R % a.HK, b = id / a.R / a.HK;
   // the first slot of sequence b: the chunks before it
-  auto tiles = [&](int i) { return i < a.B ? (kv_len(a.c, a.ctx_len, i) + a.N + KT - 1) / KT : 0; };
+  auto tiles = [&](int i) { return i < a.B ? key_tiles<KT>(a, i) : 0; };
   auto sum = [&](int c, int end) {
-    int n = 0;
-    for (int i = lane; i < end; i += WAVE) n += (tiles(i) + c - 1) / c;
+    uint32_t n = 0;
+    for (int i = lane; i < end; i += WAVE) n = add_tiles(n, (tiles(i) + c - 1) / c);
 #pragma unroll
-    for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
-    return n;
+    for (int s = 32; s > 0; s >>= 1) n = add_tiles(n, __shfl_xor(n, s, WAVE));
+    return (int)n;
   };
   const int total = sum(1, a.B);
   int c = max(1, (total + a.slots - 1) / a.slots);

@@ -44,3 +44,52 @@ def test_whole_tiles_up_to_the_last_row(ctx, D, N, G):
     torch.cuda.synchronize()
     base.check_attention(out, q, *pages, kn, vn, sees, table, [n], D ** -0.5)
     assert all(b[size:].isnan().all() for b in bufs)
+
+
+# ---------------------------------------------------------------- the last positions
+
+PAGE, WIDTH = 243, 8837381
+CAP = PAGE * WIDTH  # 2^31 - 65, the most positions that a table may have
+
+
+def last_positions_case(H, HK, D, N, seed):
+    """A table of one page again and again, with small keys, and another one last, with keys that weigh
+    as much as the new nodes'."""
+    g = torch.Generator().manual_seed(seed)
+    k = 0.02 * torch.randn(2, PAGE, HK, D, generator=g)
+    v = torch.randn(2, PAGE, HK, D, generator=g)
+    k[1] += 26 / D
+    kn = 0.02 * torch.randn(1, N, HK, D, generator=g) + 31 / D
+    vn = torch.randn(1, N, HK, D, generator=g)
+    q = 1 + 0.1 * torch.randn(1, N, H, D, generator=g)
+    table = torch.zeros(1, WIDTH, dtype=I32)
+    table[0, -1] = 1
+    return [t.to(F16) for t in (q, k, v, kn, vn)], table
+
+
+@pytest.mark.parametrize("n", [CAP, CAP - 1, CAP - 86, CAP - 130])
+@pytest.mark.parametrize("H,N,D", [(1, 3, 64), (8, 8, 64), (8, 16, 128), (32, 9, 64)])
+def test_attention_at_the_last_positions(ctx, H, N, D, n):
+    """Tiles that end beyond 2^31 keep the last cached positions and the nodes. The same page's rows
+    repeat, so the sum over them is their weights' times how often they come."""
+    (q, k, v, kn, vn), table = last_positions_case(H, 1, D, N, n % 97)
+    sees = base.sees_of(base.trees(random.Random(2), 1, N, 3))
+    out = base.run_attention(ctx, q, k, v, kn, vn, base.words_of(sees), table, [n], 1.0).cpu().double()
+    times = torch.zeros(2, PAGE, dtype=torch.float64)
+    times[0] = WIDTH - 1
+    times[1, :n - PAGE * (WIDTH - 1)] = 1
+    rows, val = k.double().flatten(0, 1)[:, 0], v.double().flatten(0, 1)[:, 0]
+    f, u = 2.0 ** -24, torch.finfo(F16).eps / 2
+    for h in range(H):
+        x = q[0, :, h].double()
+        s = torch.cat([x @ rows.t(), torch.where(sees[0], x @ kn[0, :, 0].double().t(), -torch.inf)], 1)
+        w = torch.exp(s - s.amax(1, keepdim=True)) * torch.cat([times.flatten(), torch.ones(N, dtype=torch.float64)])
+        far = w[:, :PAGE].sum(1, keepdim=True) / w.sum(1, keepdim=True)  # the repeated page's share, some 1e-4
+        assert float(far.max()) < 1e-3
+        w = w / w.sum(1, keepdim=True)
+        vals = torch.cat([val, vn[0, :, 0].double()])
+        score = x.abs() @ torch.cat([rows, kn[0, :, 0].double()]).abs().t()
+        # as elsewhere, and of the share that is summed in 2^20 steps at most: any of it
+        rel = 2 * u + 2 * (D + 4) * f * score.amax(1, keepdim=True) + 2.0 ** -16
+        tol = rel * (w @ vals.abs()) + 2 * far * vals.abs().max()
+        assert ((out[0, :, h] - w @ vals).abs() <= tol).all(), h
