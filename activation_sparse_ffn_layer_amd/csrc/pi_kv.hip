@@ -24,8 +24,8 @@ __global__ __launch_bounds__(BLOCK) void k_kv_append(AppendDev p) {
   const int len = kv_len(p.c, p.ctx_len, b);
   const int n = p.n == nullptr ? p.N : min(max(p.n[b], 0), p.N);
   if (p.len_out != nullptr && j == 0 && threadIdx.x == 0) p.len_out[b] = (int)min((long long)len + n, (long long)p.c.capacity);
-  if (j >= n || len + j >= p.c.capacity) return;
-  const int src = p.nodes == nullptr ? j : p.nodes[b * p.N + j];
+  if (j >= n || (uint32_t)len + (uint32_t)j >= (uint32_t)p.c.capacity) return;  // their sum may pass 2^31
+  const int src = p.nodes == nullptr ? j : p.nodes[(long long)b * p.N + j];
   if ((unsigned)src >= (unsigned)p.N) return;
   uint32_t off;
   const int page = kv_page(p.c, b, page_of(p.c.div, (uint32_t)(len + j), &off));

@@ -93,3 +93,26 @@ def test_attention_at_the_last_positions(ctx, H, N, D, n):
         rel = 2 * u + 2 * (D + 4) * f * score.amax(1, keepdim=True) + 2.0 ** -16
         tol = rel * (w @ vals.abs()) + 2 * far * vals.abs().max()
         assert ((out[0, :, h] - w @ vals).abs() <= tol).all(), h
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_append_at_the_last_positions(ctx, listed):
+    """Tokens beyond the table are dropped, also those whose position would pass 2^31."""
+    N, left = 200, 100
+    table = torch.zeros(2, WIDTH, dtype=I32, device=DEV)
+    table[0, -1] = table[1, 0] = 1
+    k = torch.zeros(2, PAGE, 1, 8, dtype=F16, device=DEV)
+    v = torch.zeros_like(k)
+    kn = torch.arange(1, 2 * N + 1, device=DEV).view(2, N, 1, 1).expand(2, N, 1, 8).to(F16).contiguous()
+    lens = torch.tensor([CAP - left, 7], dtype=I32, device=DEV)
+    grown = torch.zeros_like(lens)
+    nodes = torch.arange(N, dtype=I32, device=DEV).flip(0).expand(2, N).contiguous() if listed else None
+    n = torch.tensor([N, 3], dtype=I32, device=DEV)
+    pi.kv_append(ctx, pi.KvCache(ctx, k, v), kn, -kn, table, lens, grown, nodes, n)
+    torch.cuda.synchronize()
+    rows = torch.arange(N, 0, -1) if listed else torch.arange(1, N + 1)
+    want = torch.zeros(PAGE, dtype=torch.int64)
+    want[PAGE - left:] = rows[:left]
+    want[7:10] = N + rows[:3]
+    assert k[1, :, 0, 0].tolist() == want.tolist() and (k[0] == 0).all() and torch.equal(v, -k)
+    assert grown.tolist() == [CAP, 10]
