@@ -81,8 +81,10 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(NormDev p) {
   float rinv = mean > 0.f ? 1.0f / sqrtf(mean) : 0.f;  // a row of zeros, without eps: zeros
   bool bad = !(ss < __builtin_inff());
   if (bad || mean < 1e-30f) {
-    // Squares beyond fp32's range, or lost below it: again with the row's largest element near 1. A
-    // NaN makes the sum one; an infinity is its row's largest.
+    // Squares beyond fp32's range, or lost below it: again with the row times a power of two that
+    // brings its largest element, or eps's root where that is larger, near 1. The scaled row is what
+    // goes on: the root's reciprocal for the row as it is may lie beyond the range. A NaN makes the
+    // sum one; an infinity is its row's largest.
     float big = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -91,18 +93,18 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm(NormDev p) {
     big = block_fold<NW, true>(big, red[1]);
     bad = ss != ss || !(big < __builtin_inff());
     if (!bad && big > 0.f) {
-      const int e = -ilogbf(big);
+      const int e = -ilogbf(fmaxf(big, sqrtf(p.eps)));
       float s2 = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = ldexpf(h[j][i], e);
-          s2 += x * x;
+          h[j][i] = ldexpf(h[j][i], e);
+          s2 += h[j][i] * h[j][i];
         }
       __syncthreads();  // red is free again
       s2 = block_fold<NW, false>(s2, red[0]);
-      rinv = ldexpf(1.0f / sqrtf(s2 / (float)p.d + ldexpf(ldexpf(p.eps, e), e)), e);
+      rinv = 1.0f / sqrtf(s2 / (float)p.d + ldexpf(ldexpf(p.eps, e), e));
     }
     __syncthreads();
   }

@@ -28,9 +28,41 @@ def run(ctx, x, w, eps):
     return y, q, scale
 
 
+def definition(x, w, eps):
+    h = x.double()
+    return h / (h.square().mean(1, keepdim=True) + eps).sqrt() * w.double()
+
+
 def rounded(y, scale):
     """round(y / scale) of the fp32 values that the call gave, with fp32's rounding of the quotient."""
     return torch.round((y.double() / scale.double()[:, None]).float())
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-31, 1e-36, 1e-42])
+@pytest.mark.parametrize("d", [64, 4096, 20000])
+def test_tiny_rows(ctx, d, eps):
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn(7, d, generator=g)
+    x[0] *= 1e-37
+    x[1] *= 1e-38
+    x[2] *= 1e-40  # below fp32's normal range
+    x[3] = 0
+    x[3, 3] = 1e-37  # one element
+    x[4] = 0
+    x[4, d - 1] = -(2.0 ** -149)
+    x[5] *= 1e-15
+    x[6] *= 1e-17
+    x = x.to(DEV)
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(DEV)
+    y, q, scale = run(ctx, x, w, eps)
+    want = definition(x, w, float(torch.tensor(eps, dtype=F32)))
+    # as for ordinary rows (the sum of squares, half of it in the root, root, reciprocal and products)
+    rel = (21 + 6) * f
+    assert ((y.double() - want).abs() <= rel * want.abs() + 2.0 ** -150).all()
+    top = want.abs().amax(1)
+    assert ((scale.double() * 127 - top).abs() <= (rel + 2 * f) * top + 127 * 2.0 ** -150).all()
+    keep = scale > 0
+    assert (q[keep].float() == rounded(y, scale)[keep].clamp(-127, 127)).all() and (q[~keep] == 0).all()
 
 
 @pytest.mark.parametrize("tiny", [1e-36, 1e-38, 1e-40])
