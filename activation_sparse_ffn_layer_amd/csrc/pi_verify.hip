@@ -198,9 +198,11 @@ template <typename T>
 __device__ __forceinline__ const T* row_of(const VfDev& p, int b, int i) {
   return static_cast<const T*>(p.logits) + (long long)b * p.lb + (long long)i * p.ln;
 }
-__device__ __forceinline__ double inv_temp(const VfDev& p, int b) {  // log2(e) / T; 0: greedy
+// log2(e) / T; 0: greedy. An infinite temperature's is a number that no logit's distance makes visible
+// but that leaves -inf at -inf.
+__device__ __forceinline__ double inv_temp(const VfDev& p, int b) {
   const float t = p.temp == nullptr ? 1.f : p.temp[b];
-  return t > 0.f ? 1.4426950408889634 / (double)t : 0.0;
+  return t == __builtin_inff() ? 1e-300 : t > 0.f ? 1.4426950408889634 / (double)t : 0.0;
 }
 __device__ __forceinline__ VfBin* bins_of(const VfDev& p, int which, int b) {
   return p.bins + ((long long)which * p.B + b) * p.chunks;
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   const int chunk = CW == 1 ? (int)blockIdx.x * NWAVES + wave : (int)blockIdx.x, node = blockIdx.y, b = blockIdx.z;
   if (CW == 1 && chunk >= p.chunks) return;
   const double itd = inv_temp(p, b);
-  const float it = fminf((float)itd, 3e38f);
+  const float it = fmaxf(fminf((float)itd, 3e38f), 1.4e-45f);  // not 0, whose product with -inf is a NaN
   const T* row = row_of<T>(p, b, node);
   constexpr int G = VF_CH / (8 * WAVE * CW);
   const int i0 = chunk * VF_CH + (CW == 1 ? lane : (int)threadIdx.x) * 8;

@@ -387,7 +387,8 @@ pi_status pi_tree_attention(pi_ctx *ctx, pi_attn *attn, const pi_attn_args *args
  *   without q:  child t is taken where u[b][i] < r[t]; else r[t] becomes 0 and r is normalised
  * until a node has no child that is taken. The next token is then drawn from r (from p where r
  * has no weight left) at u_next[b]: the first whose running sum is above u_next * the total.
- * NaN logits count as -inf, +inf as the largest finite value; a row of nothing else but -inf
+ * An infinite temperature weighs all logits but -inf alike. NaN logits count as -inf, +inf as the
+ * largest finite value; a row of nothing else but -inf
  * gives the next token -1. Sums are in 64 bits and in a fixed order.
  *   logits     [B][N][vocab], rows need no alignment beyond the element's
  *   q          fp32 [B][N][vocab] or NULL: the draft's probabilities after each node

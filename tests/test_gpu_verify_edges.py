@@ -1,0 +1,52 @@
+"""Verification at the ends of its arguments: temperatures without bound, numbers of 1, drafts that
+all but equal the target."""
+import pytest
+import torch
+
+from tests import test_gpu_decoder as base
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import activation_sparse_ffn_layer_amd as pi
+
+DEV, F16, BF16, F32, I32 = "cuda", torch.float16, torch.bfloat16, torch.float32, torch.int32
+BIG = torch.finfo(F32).max
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return pi.Context(max_batch=1, max_d=64, max_ffn=64, max_rank=0)
+
+
+@pytest.mark.parametrize("V,dtype", [(40, F16), (9001, F32), (70001, BF16)])
+def test_infinite_temperature_is_uniform(ctx, V, dtype):
+    """Every logit that is not -inf has the same weight; NaN counts as -inf, +inf as finite."""
+    g = torch.Generator().manual_seed(V)
+    B, N = 4, 3
+    logits = (20 * torch.randn(B, N, V, generator=g)).to(dtype)
+    logits[torch.rand(B, N, V, generator=g) < 0.3] = float("-inf")
+    logits[:, :, 5] = float("nan")
+    logits[:, :, 7] = float("inf")
+    if dtype is not F16:
+        logits[:, :, 8], logits[:, :, 9] = BIG / 1.01, -BIG / 1.01
+    live = (logits > float("-inf")).double()
+    tok = torch.full((B, N), 7, dtype=I32)
+    tok[2, 1] = 5  # has no weight
+    par = torch.tensor([[-1, 0, 1]] * B, dtype=I32)
+    u = torch.zeros(B, N)
+    for b in range(B):
+        count = live[b].sum(1)
+        u[b, 1], u[b, 2] = 0.99 / count[0], (1.01 if b % 2 else 0.99) / count[1]
+    u[3, 1] = 1.01 / live[3, 0].sum()
+    u_next = torch.tensor([0.0, 0.3, 0.71, 0.9999])
+    nodes, out, n = base.run_verify(ctx, dict(logits=logits, tokens=tok, parents=par, u=u, u_next=u_next, q=None,
+                                              temp=torch.full((B,), float("inf"))))
+    assert n.tolist() == [3, 2, 1, 1]
+    for b in range(B):
+        p = live[b, int(n[b]) - 1].clone()
+        if b in (1, 3):  # a child with weight was refused
+            p[7] = 0
+        p[5] = 0
+        cum = p.cumsum(0)
+        assert int(out[b, int(n[b]) - 1]) == int((cum <= float(u_next[b]) * cum[-1]).sum()), b
