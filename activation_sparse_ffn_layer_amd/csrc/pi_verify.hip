@@ -495,7 +495,10 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
   const int chunk = CW == 1 ? (int)blockIdx.x * NWAVES + wave : (int)blockIdx.x, node = blockIdx.y, b = blockIdx.z;
   if (CW == 1 && chunk >= p.chunks) return;
   const double itd = inv_temp(p, b);
-  const float it = fmaxf(fminf((float)itd, 3e38f), 1.4e-45f);  // not 0, whose product with -inf is a NaN
+  // Twice log2(e) / T, not 0, whose product with -inf is a NaN, for half the distance of a logit from the
+  // maximum: that of two finite logits may lie beyond fp32's range where a hot row's weights do not.
+  const float it2 = fmaxf(fminf((float)(2.0 * itd), 3e38f), 1.4e-45f);
+  auto weight = [&](float z, float m) { return __builtin_amdgcn_exp2f(__builtin_fmaf(z, 0.5f, -0.5f * m) * it2); };
   const T* row = row_of<T>(p, b, node);
   constexpr int G = VF_CH / (8 * WAVE * CW);
   const int i0 = chunk * VF_CH + (CW == 1 ? lane : (int)threadIdx.x) * 8;
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[j & 3] += __builtin_amdgcn_exp2f((z(g, j) - m) * it);
+        for (int j = 0; j < 8; ++j) part[j & 3] += weight(z(g, j), m);
       sum = wave_sum((part[0] + part[1]) + (part[2] + part[3]));
     } else {
 #pragma unroll
@@ -553,7 +556,7 @@ __global__ __launch_bounds__(BLOCK) void k_verify_rows(VfDev p) {
     o.s = 0.f;
 #pragma unroll
     for (int k = 0; k < CW; ++k)
-      if (w[k].s > 0.f) o.s += w[k].s * __builtin_amdgcn_exp2f((w[k].m - o.m) * it);
+      if (w[k].s > 0.f) o.s += w[k].s * weight(w[k].m, o.m);
   }
   if (CW == 1 ? lane == 0 : true) p.part[((long long)b * p.N + node) * p.chunks + chunk] = o;
 }

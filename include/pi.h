@@ -388,8 +388,8 @@ pi_status pi_tree_attention(pi_ctx *ctx, pi_attn *attn, const pi_attn_args *args
  * until a node has no child that is taken. The next token is then drawn from r (from p where r
  * has no weight left) at u_next[b]: the first whose running sum is above u_next * the total.
  * An infinite temperature weighs all logits but -inf alike. NaN logits count as -inf, +inf as the
- * largest finite value; a row of nothing else but -inf
- * gives the next token -1. Sums are in 64 bits and in a fixed order.
+ * largest finite value; a row of nothing else but -inf gives the next token -1. Sums are in
+ * 64 bits and in a fixed order.
  *   logits     [B][N][vocab], rows need no alignment beyond the element's
  *   q          fp32 [B][N][vocab] or NULL: the draft's probabilities after each node
  *   tokens, parents  device int32 [B][N]; a parent outside [0, i) keeps node i off every path

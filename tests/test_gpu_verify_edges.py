@@ -50,3 +50,22 @@ def test_infinite_temperature_is_uniform(ctx, V, dtype):
         p[5] = 0
         cum = p.cumsum(0)
         assert int(out[b, int(n[b]) - 1]) == int((cum <= float(u_next[b]) * cum[-1]).sum()), b
+
+
+@pytest.mark.parametrize("with_q", [True, False])
+def test_hot_rows_of_the_largest_logits(ctx, with_q):
+    """Logits at both ends of fp32's range: their difference is beyond it, their weights are not."""
+    B, N, V = 8, 4, 6000
+    g = torch.Generator().manual_seed(2)
+    logits = torch.where(torch.rand(B, N, V, generator=g) < 0.5, BIG, -BIG)
+    logits[:, :, :4] = BIG
+    q = torch.softmax(torch.randn(B, N, V, generator=g), 2) if with_q else None
+    tok = torch.tensor([[0, 1, 2, 3]] * B, dtype=I32)
+    par = torch.tensor([[-1, 0, 0, 1]] * B, dtype=I32)
+    temp = torch.full((B,), 3e38)
+    u = torch.rand(B, N, generator=g) * 2e-4
+    for b in range(B):  # next to the first child's border, by 4%
+        p = torch.softmax((logits[b, 0].double() - BIG) / float(temp[b]), 0)[1]
+        u[b, 1] = (p if q is None else p / q[b, 0, 1]) * (0.96 if b % 2 else 1.04)
+    c = dict(logits=logits, tokens=tok, parents=par, u=u, u_next=torch.rand(B, generator=g), q=q, temp=temp)
+    base.check_verify(base.run_verify(ctx, c), c)
