@@ -451,7 +451,8 @@ __device__ __forceinline__ void walk(const VfDev& p, VfShared& s, int b, double 
         break;
       }
       next = i + 1;
-      const bool take = !again && lhs < rhs;
+      // without a q no probability is above 1, whatever the roundings of what is left of it
+      const bool take = !again && lhs < rhs && (p.q != nullptr || u < 1.0);
       if (take) {
         cur = i;
         c = 0.0;
@@ -469,7 +470,7 @@ __device__ __forceinline__ void walk(const VfDev& p, VfShared& s, int b, double 
           break;
         }
       } else if (!again) {
-        left -= pt;
+        left = fmax(left - pt, 0.0);
       }
       g = next / WAVE;
     }

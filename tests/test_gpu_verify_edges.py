@@ -69,3 +69,17 @@ def test_hot_rows_of_the_largest_logits(ctx, with_q):
         u[b, 1] = (p if q is None else p / q[b, 0, 1]) * (0.96 if b % 2 else 1.04)
     c = dict(logits=logits, tokens=tok, parents=par, u=u, u_next=torch.rand(B, generator=g), q=q, temp=temp)
     base.check_verify(base.run_verify(ctx, c), c)
+
+
+def test_numbers_of_one_take_nothing(ctx):
+    """Without a q: no probability is above 1, and what is left of 1 after all refusals is nothing."""
+    B, N, V = 256, 5, 50
+    g = torch.Generator().manual_seed(4)
+    logits = torch.full((B, N, V), float("-inf"))
+    logits[:, :, :3] = torch.randn(B, N, 3, generator=g)
+    tok = torch.tensor([[0, 0, 1, 2, 9]] * B, dtype=I32)  # the fourth child's token has no weight
+    par = torch.tensor([[-1, 0, 0, 0, 0]] * B, dtype=I32)
+    c = dict(logits=logits, tokens=tok, parents=par, u=torch.ones(B, N), u_next=torch.rand(B, generator=g), q=None, temp=None)
+    nodes, out, n = base.run_verify(ctx, c)
+    assert n.tolist() == [1] * B and (nodes[:, 1:] == -1).all()
+    assert ((out[:, 0] >= 0) & (out[:, 0] < 3)).all()
