@@ -216,6 +216,7 @@ struct VfShared {
   VfBin red[VF_NT / WAVE];
   double target, before;
   int32_t pick, last;
+  int32_t again;      // the residual's weight is needed once more, now that Z is known in 64 bits
 };
 
 // 8 tokens of the current row from i on: exp((z - m) / T), the draft's q (0 without one), and a bit
@@ -291,14 +292,19 @@ __device__ __forceinline__ VfBin first_bin(const VfDev& p, const VfBin* bins) {
   return (int)threadIdx.x < p.chunks ? bins[threadIdx.x] : VfBin{0.0, 0.0, 0.0};
 }
 
-// The sums of the pass that the walk waited for: Z and the residual's weight. `v`: first_bin.
+// The sums of the pass that the walk waited for: Z and the residual's weight. `v`: first_bin. The tokens
+// of the residual were chosen by the 32-bit Z. The error of that Z, relative to Z, bounds what wrongly
+// chosen tokens weigh: nothing beside the residual, but where the draft is the target to within a few
+// roundings. A residual below 2^20 times the error is summed again, by the 64-bit Z.
 template <int NT>
 __device__ __forceinline__ void join_bins(const VfDev& p, VfShared& s, const VfBin* bins, VfBin v) {
   for (int k = threadIdx.x + NT; k < p.chunks; k += NT) v = VfBin{v.e + bins[k].e, v.a + bins[k].a, v.q + bins[k].q};
   v = block_sum<NT>(v, s.red);
   if (threadIdx.x == 0) {
+    const double left = s.st.c > 0.0 ? fmax(v.a / v.e - s.st.c * v.q, 0.0) : 1.0;
+    s.again = s.st.z == 0.0 && s.st.c > 0.0 && left < 0x1p20 * fabs(s.rs[s.st.cur] / v.e - 1.0);
     s.st.z = v.e;
-    s.st.left = s.st.c > 0.0 ? fmax(v.a / v.e - s.st.c * v.q, 0.0) : 1.0;
+    s.st.left = left;
   }
   __syncthreads();
 }
@@ -683,7 +689,7 @@ __global__ __launch_bounds__(VF_NT) void k_verify_pass(VfDev p, int pass) {
       return;
     }
     join_bins<NT>(p, s, bins_of(p, src, b), v);
-    walk(p, s, b, it, src, first);
+    if (!s.again) walk(p, s, b, it, src, first);
   }
   if (first && threadIdx.x == 0) *now = s.st;
   if (s.st.stage >= DONE) return;
@@ -698,7 +704,7 @@ __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
   const double it = inv_temp(p, b);
   load_state(p, s, b, passes);
   int src = (passes - 1) & 1;
-  // at most one round per node and one more per row: each consumes a child or settles a row's sum
+  // at most one round per node and two more per row: each consumes a child or settles a row's sum
   while (s.st.stage < DONE) {
     if (s.st.stage == WAIT_DRAW) {
       __syncthreads();
@@ -707,7 +713,7 @@ __global__ __launch_bounds__(VF_NT) void k_verify_end(VfDev p, int passes) {
       break;
     }
     join_bins<VF_NT>(p, s, bins_of(p, src, b), first_bin(p, bins_of(p, src, b)));
-    walk(p, s, b, it, src, true);
+    if (!s.again) walk(p, s, b, it, src, true);
     if (s.st.stage >= DONE) break;
     src = 2;
     for (int k = threadIdx.x / WAVE; k < p.chunks; k += VF_NT / WAVE) {

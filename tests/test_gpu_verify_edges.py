@@ -83,3 +83,22 @@ def test_numbers_of_one_take_nothing(ctx):
     nodes, out, n = base.run_verify(ctx, c)
     assert n.tolist() == [1] * B and (nodes[:, 1:] == -1).all()
     assert ((out[:, 0] >= 0) & (out[:, 0] < 3)).all()
+
+
+@pytest.mark.parametrize("V,N", [(3000, 2), (5000, 12), (66001, 3)])
+def test_draft_that_all_but_equals_the_target(ctx, V, N):
+    """q is p rounded to fp32, but for the first child's token: what is left after its refusal are the
+    roundings, which only a sum in 64 bits tells apart."""
+    B = 16
+    g = torch.Generator().manual_seed(V)
+    logits = torch.randn(B, N, V, generator=g)
+    q = torch.softmax(logits.double(), 2).float()
+    tok = torch.randint(0, V, (B, N), generator=g, dtype=I32)
+    par = torch.zeros(B, N, dtype=I32)
+    par[:, 0] = -1
+    for b in range(B):
+        q[b, 0, int(tok[b, 1])] *= 1.05
+        tok[b, 2:] = tok[b, 1]
+    c = dict(logits=logits, tokens=tok, parents=par, u=torch.full((B, N), 0.999), u_next=torch.rand(B, generator=g), q=q,
+             temp=None)
+    base.check_verify(base.run_verify(ctx, c), c)
