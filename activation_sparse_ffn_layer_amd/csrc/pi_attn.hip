@@ -30,7 +30,7 @@ using namespace pi;
 
 struct pi_attn {
   pi_ctx* ctx;
-  const pi_kv* kv;
+  pi_kv kv;         // a copy: the cache's handle may be destroyed before this one
   int heads, max_batch, max_nodes;
   float scale;
   uint8_t* ws;
@@ -740,12 +740,13 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
       return fail(ctx, PI_ERR_HIP, "filling the attention scratch failed");
     }
   }
-  pi_attn* a = new (std::nothrow) pi_attn{ctx, kv, heads, max_batch, max_nodes, scale, ws, reinterpret_cast<float*>(ws),
+  pi_attn* a = new (std::nothrow) pi_attn{ctx, *kv, heads, max_batch, max_nodes, scale, ws, reinterpret_cast<float*>(ws),
                                           reinterpret_cast<float*>(ws + ob), self};
   if (a == nullptr) {
     (void)hipFree(ws);
     return fail(ctx, PI_ERR_OOM, "host allocation failed");
   }
+  ctx_retain(ctx);
   *out = a;
   return PI_OK;
 }
@@ -754,6 +755,7 @@ void pi_attn_destroy(pi_attn* attn) {
   if (attn == nullptr) return;
   (void)hipSetDevice(attn->ctx->device);
   (void)hipFree(attn->ws);
+  ctx_release(attn->ctx);
   delete attn;
 }
 
@@ -763,7 +765,7 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
   if (attn->ctx != ctx) return fail(ctx, PI_ERR_INVALID, "attn belongs to another context");
   if (args == nullptr) return fail(ctx, PI_ERR_INVALID, "args is NULL");
   const pi_attn_args& a = *args;
-  const pi_kv* kv = attn->kv;
+  const pi_kv* kv = &attn->kv;
   PI_TRY(check_paging(ctx, kv, a.table, a.table_stride, a.table_width, a.ctx_len, a.B, a.N));
   if (a.B > attn->max_batch || a.N > attn->max_nodes)
     return fail(ctx, PI_ERR_INVALID, "B %d, N %d above the handle's %d, %d", a.B, a.N, attn->max_batch, attn->max_nodes);

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <hip/hip_ext.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -15,6 +16,7 @@
 using pi::half_t;
 
 struct pi_ctx {
+  std::atomic<int> refs{1};  // its creator's until pi_ctx_destroy, and one of each handle
   int device = 0;
   hipStream_t stream = nullptr;
   int max_batch = 0, max_d = 0, max_ffn = 0, max_rank = 0;
@@ -78,6 +80,13 @@ inline pi_status fail(pi_ctx* ctx, pi_status s, const char* fmt, ...) {
     hipError_t e_ = (call);                                                                      \
     if (e_ != hipSuccess) return fail((ctx), PI_ERR_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
   } while (0)
+
+// A handle refers to its context until it is destroyed itself, in whatever order: what
+// pi_ctx_destroy leaves is an empty context at an address that no other one takes.
+inline void ctx_retain(pi_ctx* c) { c->refs.fetch_add(1); }
+inline void ctx_release(pi_ctx* c) {
+  if (c->refs.fetch_sub(1) == 1) delete c;
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -71,11 +71,16 @@ pi_status pi_kv_create(pi_ctx* ctx, const pi_kv_desc* desc, pi_kv** out) {
   PI_TRY(check_dev_ptr(ctx, d.v, "v"));
   pi_kv* kv = new (std::nothrow) pi_kv{d, ctx};
   if (kv == nullptr) return fail(ctx, PI_ERR_OOM, "host allocation failed");
+  ctx_retain(ctx);
   *out = kv;
   return PI_OK;
 }
 
-void pi_kv_destroy(pi_kv* kv) { delete kv; }
+void pi_kv_destroy(pi_kv* kv) {
+  if (kv == nullptr) return;
+  ctx_release(kv->ctx);
+  delete kv;
+}
 
 pi_status pi_kv_append(pi_ctx* ctx, const pi_kv* kv, const pi_append_args* args) {
   if (ctx == nullptr) return PI_ERR_INVALID;

@@ -1027,12 +1027,12 @@ pi_status pi_ctx_create(int32_t device, void* hip_stream, int32_t max_batch, int
 void pi_ctx_destroy(pi_ctx* ctx) {
   if (ctx == nullptr) return;
   (void)hipSetDevice(ctx->device);
-  if (ctx->gexec != nullptr) (void)hipGraphExecDestroy(ctx->gexec);
+  drop_graph(ctx);
   if (ctx->cap_stream != nullptr) (void)hipStreamDestroy(ctx->cap_stream);
   for (hipEvent_t e : ctx->ev) (void)hipEventDestroy(e);
   if (ctx->ws != nullptr) (void)hipFree(ctx->ws);
   if (ctx->lin_part != nullptr) (void)hipFree(ctx->lin_part);
-  delete ctx;
+  ctx_release(ctx);
 }
 
 pi_status pi_ctx_set_stream(pi_ctx* ctx, void* hip_stream) {
@@ -1060,6 +1060,7 @@ pi_status pi_ffn_create(pi_ctx* ctx, const pi_ffn_desc* desc, pi_ffn** out) {
   if (f == nullptr) return fail(ctx, PI_ERR_OOM, "host allocation failed");
   f->desc = d;
   f->ctx = ctx;
+  ctx_retain(ctx);
   f->serial = g_ffn_serial.fetch_add(1);
   *out = f;
   return PI_OK;
@@ -1069,10 +1070,11 @@ void pi_ffn_destroy(pi_ffn* ffn) {
   if (ffn == nullptr) return;
   // a captured stack step holding this layer's pointers is dropped with it
   pi_ctx* c = ffn->ctx;
-  if (c != nullptr && std::find(c->g_layers.begin(), c->g_layers.end(), ffn->serial) != c->g_layers.end()) {
+  if (std::find(c->g_layers.begin(), c->g_layers.end(), ffn->serial) != c->g_layers.end()) {
     (void)hipSetDevice(c->device);
     drop_graph(c);
   }
+  ctx_release(c);
   delete ffn;
 }
 

@@ -437,11 +437,16 @@ pi_status pi_linear_create(pi_ctx* ctx, const pi_linear_desc* desc, pi_linear** 
   }
   pi_linear* l = new (std::nothrow) pi_linear{ctx, d};
   if (l == nullptr) return fail(ctx, PI_ERR_OOM, "host allocation failed");
+  ctx_retain(ctx);
   *out = l;
   return PI_OK;
 }
 
-void pi_linear_destroy(pi_linear* lin) { delete lin; }
+void pi_linear_destroy(pi_linear* lin) {
+  if (lin == nullptr) return;
+  ctx_release(lin->ctx);
+  delete lin;
+}
 
 pi_status pi_linear_q8(pi_ctx* ctx, pi_linear* lin, const int8_t* x, int64_t x_stride, const float* x_scale, int32_t M,
                        void* y, int32_t y_dtype, int64_t y_stride) {

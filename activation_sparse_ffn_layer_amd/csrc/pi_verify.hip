@@ -775,6 +775,7 @@ pi_status pi_verifier_create(pi_ctx* ctx, int32_t vocab, int32_t max_batch, int3
     (void)hipFree(ws);
     return fail(ctx, PI_ERR_OOM, "host allocation failed");
   }
+  ctx_retain(ctx);
   *out = v;
   return PI_OK;
 }
@@ -783,6 +784,7 @@ void pi_verifier_destroy(pi_verifier* ver) {
   if (ver == nullptr) return;
   (void)hipSetDevice(ver->ctx->device);
   (void)hipFree(ver->ws);
+  ctx_release(ver->ctx);
   delete ver;
 }
 

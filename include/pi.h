@@ -107,7 +107,9 @@ const char *pi_last_error(const pi_ctx *ctx);
 
 /* Create a context bound to `device` and the HIP stream `hip_stream` (hipStream_t, may be
  * NULL for the default stream). Sizes the scratch for batches up to max_batch tokens and
- * layers up to max_d x max_ffn with predictor rank up to max_rank. Allocates device memory. */
+ * layers up to max_d x max_ffn with predictor rank up to max_rank. Allocates device memory.
+ * A context and its handles may be destroyed in any order; no call takes a handle once its
+ * context is destroyed. */
 pi_status pi_ctx_create(int32_t device, void *hip_stream, int32_t max_batch, int32_t max_d,
                         int32_t max_ffn, int32_t max_rank, pi_ctx **out);
 void pi_ctx_destroy(pi_ctx *ctx);
@@ -291,7 +293,8 @@ pi_status pi_permute_rows(pi_ctx *ctx, const void *src, void *dst, const int32_t
  * They follow the conventions above. Tensors of these calls may be views: strides are given
  * in elements, the last axis is contiguous, and rows start at a multiple of 16 bytes unless a
  * call says otherwise. A handle (pi_kv, pi_attn, pi_verifier, pi_linear) keeps its own scratch,
- * sized when it is created, and borrows the pointers of its description. */
+ * sized when it is created, and borrows the pointers of its description. A pi_attn keeps its
+ * cache's description and pointers, not the pi_kv. */
 
 typedef enum { PI_T_F32 = 0, PI_T_F16 = 1, PI_T_BF16 = 2 } pi_dtype;
 
