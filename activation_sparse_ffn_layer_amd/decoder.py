@@ -61,6 +61,13 @@ def _view(t, name: str, dtype, shape, device: int):
     _refuse(t, name, dtype, shape, device)
 
 
+def _common(sa, sb, shape, names: str):
+    """Strides that two tensors of this shape share: a stride along one element means nothing."""
+    if sa != sb and any(a != b and n != 1 for a, b, n in zip(sa, sb, shape)):
+        _bad(f"{names} need equal strides")
+    return sa
+
+
 def _borrow(ctx, *tensors):
     """Keep the tensors' memory from reuse until the context's stream is done with them, where
     that is not the stream they are used on otherwise."""
@@ -97,8 +104,7 @@ class KvCache(_Handle):
             _bad("k must be an fp16 or bf16 tensor [pages][page_tokens][heads][head_dim]")
         pk, sk = _view(k, "k", k.dtype, k.shape, ctx.device)
         pv, sv = _view(v, "v", k.dtype, k.shape, ctx.device)
-        if sk != sv:
-            _bad("k and v need equal strides")
+        sk = _common(sk, sv, k.shape, "k and v")
         self.ctx, self.k, self.v, self.dtype = ctx, k, v, k.dtype
         self.pages, self.page_tokens, self.heads, self.head_dim = k.shape
         desc = KvDesc(DTYPE[k.dtype], self.heads, self.head_dim, self.pages, self.page_tokens, pk, pv, sk[0], sk[1], sk[2])
@@ -120,9 +126,7 @@ def _new_kv(cache: KvCache, k_new, v_new, B: int, N: int, device: int):
     shape = (B, N, cache.heads, cache.head_dim)
     pk, sk = _view(k_new, "k_new", cache.dtype, shape, device)
     pv, sv = _view(v_new, "v_new", cache.dtype, shape, device)
-    if sk != sv:
-        _bad("k_new and v_new need equal strides")
-    return pk, pv, sk
+    return pk, pv, _common(sk, sv, shape, "k_new and v_new")
 
 
 def kv_append(ctx, cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, table: Optional[torch.Tensor],
