@@ -60,8 +60,8 @@ def parse():
     return ap.parse_args()
 
 
-# what the stack's kernels and launches are built from
-STACK_SOURCES = ("pi_device.hpp", "pi_kernels.hpp", "pi_lib.hip", "pi_mfma.hpp")
+# what the stack's kernels and launches are built from: pi_lib.hip and what it includes
+STACK_SOURCES = ("pi_device.hpp", "pi_host.hpp", "pi_kernels.hpp", "pi_lib.hip", "pi_mfma.hpp")
 
 
 def kernel_source_hash():
