@@ -388,16 +388,22 @@ int split_count(int cus, int tiles, int K) {
   return std::max(1, std::min(2 * cus / tiles, (K + LT_K - 1) / LT_K / 4));
 }
 
-// Up to 16 tokens each workgroup of k_q8_rows reads all of x, which a tile reads once for 128 rows:
-// at K = 8192 and N = 10240 the rows take 20.1 us at one token, 23.1 at 8 and 27.1 at 16, tiles
-// some 20.5; at K = 4096 and N = 12288 11.9, 13.3 and 14.8 against 15.5.
-bool by_rows(int M, int K) { return M == 1 || (M <= 16 && M * K < 65536); }
+// Up to 16 tokens. Each workgroup of k_q8_rows reads all of x, which costs 4.4 us per 10^9 of M N K (the
+// same at all six shapes measured); tiles read it once for 128 rows, but join their ranges' sums, 2 to
+// 5 us. Rows against tiles, us: K = 4096, N = 12288: 12.1 / 17.1 at one token, 15.4 / 17.8 at 16;
+// K = 8192, N = 10240: 20.6 / 21.7 at 2, 22.2 / 22.0 at 6, 26.9 / 22.9 at 16; K = 4096, N = 32000:
+// 29.7 / 30.5 at 6, 34.2 / 31.2 at 12; K = 8192, N = 28672: 46.5 / 48.0 at 3, 51.9 / 49.0 at 8. Few rows
+// of great length leave most CUs without any: K = 16384, N = 1024: 12.8 / 11.4 at 2, 17.2 / 12.2 at 16,
+// but K = 8192, N = 1024: 8.8 / 9.3 at 8. One token has no use for tiles, nor their scratch.
+bool by_rows(int M, int N, int K) {
+  return M == 1 || (M <= 16 && (long long)M * N * K < 850000000 && K <= 8ll * N);
+}
 
 template <typename T>
 pi_status launch_linear(pi_ctx* c, const LinDev& p) {
   // 4 outputs in one store where every row starts at such a boundary
   const bool wide = p.y_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-  if (by_rows(p.M, p.K)) {
+  if (by_rows(p.M, p.N, p.K)) {
     PI_HIP(c, launch_kb(c, 0, k_q8_rows<T, 1, 1>, dim3((p.N + 15) / 16), 64 * LR_WAVES, 0, p, wide));
     return PI_OK;
   }
