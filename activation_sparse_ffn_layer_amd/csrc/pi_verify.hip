@@ -733,12 +733,15 @@ pi_status launch_verify(pi_ctx* c, const VfDev& p) {
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, 1>, dim3((p.chunks + NWAVES - 1) / NWAVES, p.N, p.B), 0, p));
   else
     PI_HIP(c, launch_k(c, 0, k_verify_rows<T, NWAVES>, dim3(p.chunks, p.N, p.B), 0, p));
-  // A pass costs 2.7 us where it finds nothing to do and some 7 where it does; what is left after them
-  // the last kernel does at 63 us a residual of 131072 tokens and 17 of 32000, on one CU. A path
-  // has few rejections; trees of more nodes and batches of more sequences are likelier to have
-  // one with many (16 trees of 32 nodes: 82 to 87 us with 4 passes, 88 to 92 with 6, none left
-  // over in either). Without a q one pass is enough but for tests too near to call.
-  const int most = p.chunks > 16 ? (p.B > 16 ? 6 : 4) : p.N > 8 ? 4 : 2;
+  // A pass costs some 2 us where it finds nothing to do; what is left after the last one k_verify_end does
+  // on one CU, at 63 us a residual of 131072 tokens and 12 of 32000. The more nodes there are in all, the
+  // likelier is a path with many rejections. Means over 36 draws (the longest of them), us, with 2, 4 and
+  // 6 passes: one chain of 5, 32000 tokens: 31.9, 35.5 (all that it can take); one tree of 16: 34.4, 37.9,
+  // 41.5; 131072 tokens: 39.8 (105), 40.0 (47), 43.8; one tree of 32, 32000 tokens: 35.8 (94), 38.3 (70),
+  // 41.6 (60); 4 trees of 32: 45.8, 44.6, 48.4; 131072 tokens: 76 (187), 51 (62), 56; 16 of 32: 150 (223),
+  // 81 (89), 86; 32 of 32: 202, 127, 132; 8 of 64: 162 (279), 91 (162), 85 (95); 64 of 8: 147, 106, 113.
+  // Without a q one pass is enough but for tests too near to call.
+  const int most = p.N * p.B > 16 ? 4 : 2;
   const int passes = p.q == nullptr ? 1 : std::min(most, std::max(1, p.N - 1));
   PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, true>, dim3(p.chunks, p.B), VF_NT, 0, p, 0));
   for (int i = 1; i < passes; ++i) PI_HIP(c, launch_kb(c, 0, k_verify_pass<T, false>, dim3(p.chunks, p.B), VF_NT, 0, p, i));
