@@ -241,7 +241,8 @@ def add_rmsnorm(ctx, x: torch.Tensor, res: Optional[torch.Tensor], w: torch.Tens
 
 class Linear(_Handle):
     """A pi_linear: an 8-bit weight ``w`` [N][K] (int8, borrowed) with a scale per output channel and
-    an optional fp32 bias, for up to ``max_tokens`` tokens."""
+    an optional fp32 bias, for up to ``max_tokens`` tokens. The products of a context share its scratch:
+    graphs that hold some of them are replayed one after another."""
 
     _destroy = "pi_linear_destroy"
 

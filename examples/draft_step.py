@@ -30,16 +30,17 @@ def quantize_rows(w):
 
 class Decoder:
     """A small decoder: ``layers`` layers of width d around sparse FFNs, ``nodes`` drafted nodes for each
-    of ``batch`` sequences per step, a paged cache of ``pages`` pages per layer."""
+    of ``batch`` sequences per step, a paged cache of ``pages`` pages per layer. It works on the stream that
+    is current when it is made: torch's steps between the operators have to run there too."""
 
     def __init__(self, layers=2, d=1024, heads=16, kv_heads=4, vocab=8000, batch=2, nodes=8, page=16, pages=64, seed=0,
-                 device="cuda", stream=None):
+                 device="cuda"):
         g = torch.Generator(device).manual_seed(seed)
         randn = lambda *s: torch.randn(*s, generator=g, device=device)  # noqa: E731
         self.d, self.heads, self.kv_heads, self.dim, self.vocab = d, heads, kv_heads, d // heads, vocab
         self.batch, self.nodes, self.T, self.device = batch, nodes, batch * nodes, device
         cfg = dataclasses.replace(CONFIGS["opt6.7b"], d=d, ffn=4 * d, rank=512)
-        self.ctx = pi.Context(max_batch=self.T, max_d=d, max_ffn=cfg.ffn, max_rank=cfg.rank, stream=stream)
+        self.ctx = pi.Context(max_batch=self.T, max_d=d, max_ffn=cfg.ffn, max_rank=cfg.rank)
         qkv = (heads + 2 * kv_heads) * self.dim
         product = lambda n, k: pi.Linear(self.ctx, *quantize_rows(randn(n, k) / k ** 0.5), max_tokens=self.T)  # noqa: E731
         self.embed = randn(vocab, d).to(F16)

@@ -292,9 +292,11 @@ pi_status pi_permute_rows(pi_ctx *ctx, const void *src, void *dst, const int32_t
  * distribution, the residual's RMS norm with an 8-bit output, and the 8-bit matrix product.
  * They follow the conventions above. Tensors of these calls may be views: strides are given
  * in elements, the last axis is contiguous, and rows start at a multiple of 16 bytes unless a
- * call says otherwise. A handle (pi_kv, pi_attn, pi_verifier, pi_linear) keeps its own scratch,
- * sized when it is created, and borrows the pointers of its description. A pi_attn keeps its
- * cache's description and pointers, not the pi_kv. */
+ * call says otherwise. A pi_attn and a pi_verifier keep their own scratch, sized when they are
+ * created. The product's scratch is the context's, one buffer of 33.5 MB that all its pi_linear
+ * share: as for the FFN's calls, they and the replays of graphs that hold them must be ordered.
+ * Every handle borrows the pointers of its description; a pi_attn keeps its cache's description
+ * and pointers, not the pi_kv. */
 
 typedef enum { PI_T_F32 = 0, PI_T_F16 = 1, PI_T_BF16 = 2 } pi_dtype;
 
@@ -420,8 +422,9 @@ pi_status pi_verify(pi_ctx *ctx, pi_verifier *ver, const pi_verify_args *args);
 /* The residual's addition and RMS norm, with the norm in 8 bits, for T rows of d:
  *   res_out = round(x + res)            to res's type (x's, where res is NULL)
  *   y       = res_out / sqrt(mean(res_out^2) + eps) * w      in fp32
- *   scale   = max |y| / 127,  q = round(y / scale)           (0 and 0 for a row of zeros)
- *   x, res, res_out  any pi_dtype (res_out has res's; it may be x or res itself)
+ *   scale   = max |y| / 127,  q = round(y / scale)           (0 and 0 for a row of zeros, NaN and 0
+ *             for one with an infinity or a NaN)
+ *   x, res, res_out  any pi_dtype (res_out has res's; it may be x or res itself, of its own type)
  *   w          fp32 [d]; d a multiple of 8 up to 32768
  *   q, scale   int8 [T][d] (rows 8-byte aligned) and fp32 [T], both or neither
  *   y          [T][d] of y_dtype, nullable
@@ -448,7 +451,8 @@ pi_status pi_add_rmsnorm(pi_ctx *ctx, const pi_norm_args *args);
  *   w          int8 [N][K], w_stride elements between rows (a multiple of 16 below 2^22); K a multiple of
  *              16 below 131072 (the sums are exact in 32 bits)
  *   w_scale    fp32 [N]; bias fp32 [N] or NULL
- *   max_tokens limit of M, which sizes the scratch */
+ *   max_tokens limit of M; above 1 the context's scratch for sums of ranges of K is allocated
+ *              (once, of a size that serves every M, N and K) */
 typedef struct pi_linear_desc {
   int32_t N, K;
   const int8_t *w;
