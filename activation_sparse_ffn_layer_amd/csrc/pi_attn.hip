@@ -97,8 +97,14 @@ template <int KT>
 __device__ __forceinline__ int tile_from_end(int tile, int len) {
   return (int)((uint32_t)tile * (uint32_t)KT - (uint32_t)len);
 }
-// Sums of tiles over sequences stop at 2^30, far above the slots that they are compared with.
-__device__ __forceinline__ uint32_t add_tiles(uint32_t a, uint32_t b) { return min(a + b, 1u << 30); }
+// A sum over all sequences of what each lane adds up: a lane's stops at 2^25, above any number of slots
+// that it is compared with, so that 64 of them stay below 2^32.
+__device__ __forceinline__ uint32_t lane_tiles(uint32_t n, uint32_t more) { return min(n + more, 1u << 25); }
+__device__ __forceinline__ uint32_t sum_tiles(uint32_t n) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
+  return n;
+}
 
 // Where chunk `slot` lies: sequence b, its tiles [t0, t1), its number of chunks and the first
 // one's slot; false past the last chunk. Chunks are `c` tiles long, the least c that needs no
@@ -117,15 +123,13 @@ __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o)
   }
   const int mine = tiles(lane);  // the sequence of this lane; more than 64 are read again
   auto sum = [&](int c) {
-    uint32_t n = lane < a.B ? (mine + c - 1) / c : 0;
-    for (int b = lane + WAVE; b < a.B; b += WAVE) n = add_tiles(n, (tiles(b) + c - 1) / c);
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) n = add_tiles(n, __shfl_xor(n, s, WAVE));
-    return (int)n;
+    uint32_t n = lane_tiles(lane < a.B ? (mine + c - 1) / c : 0, 0);
+    for (int b = lane + WAVE; b < a.B; b += WAVE) n = lane_tiles(n, (tiles(b) + c - 1) / c);
+    return sum_tiles(n);
   };
-  const int total = sum(1);
-  int c = max(1, (total + a.slots - 1) / a.slots);
-  while (c > 1 && sum(c) > a.slots) c += max(1, c >> 5);
+  const uint32_t slots = (uint32_t)a.slots;
+  int c = max(1, (int)((sum(1) + slots - 1) / slots));
+  while (c > 1 && sum(c) > slots) c += max(1, c >> 5);
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += WAVE) {
     const int tl = b0 == 0 ? mine : tiles(b0 + lane);
@@ -587,15 +591,13 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
   auto tiles = [&](int i) { return i < a.B ? key_tiles<KT>(a, i) : 0; };
   auto sum = [&](int c, int end) {
     uint32_t n = 0;
-    for (int i = lane; i < end; i += WAVE) n = add_tiles(n, (tiles(i) + c - 1) / c);
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) n = add_tiles(n, __shfl_xor(n, s, WAVE));
-    return (int)n;
+    for (int i = lane; i < end; i += WAVE) n = lane_tiles(n, (tiles(i) + c - 1) / c);
+    return sum_tiles(n);
   };
-  const int total = sum(1, a.B);
-  int c = max(1, (total + a.slots - 1) / a.slots);
-  while (c > 1 && sum(c, a.B) > a.slots) c += max(1, c >> 5);
-  const int first = sum(c, b), count = (tiles(b) + c - 1) / c;
+  const uint32_t slots = (uint32_t)a.slots;
+  int c = max(1, (int)((sum(1, a.B) + slots - 1) / slots));
+  while (c > 1 && sum(c, a.B) > slots) c += max(1, c >> 5);
+  const int first = (int)sum(c, b), count = (tiles(b) + c - 1) / c;
   if (count == 1) return;
   const long long at0 = ((long long)first * a.HK + hk) * a.R + r, next = (long long)a.HK * a.R;
   float m = -__builtin_inff();
@@ -613,7 +615,8 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
     // a lane's chunk of these 64: its factor and its part of the sum
     const bool in = s0 + lane < count;
     const long long at = at0 + (in ? s0 + lane : 0) * next;
-    const float f = in ? __builtin_amdgcn_exp2f(a.ml[2 * at] - base) : 0.f;
+    // not 0 for a chunk of this sequence: an infinity that its row sees stays one, whatever it weighs
+    const float f = in ? fmaxf(__builtin_amdgcn_exp2f(a.ml[2 * at] - base), 1.4e-45f) : 0.f;
     l += in ? a.ml[2 * at + 1] * f : 0.f;
     const int n = min(WAVE, count - s0);
     for (int s = 0; s < n; s += 8) {
@@ -626,13 +629,9 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
         const int c = s + HALVES * u + mine;
         // the halves ask different lanes: what is shuffled must not depend on the asking lane's c
         const float g = __shfl(f, min(c, n - 1), WAVE);
-        // Selected, not multiplied by zero: a part may hold an infinity that the row sees, which stays one
-        // whatever its chunk weighs.
+        // past the last chunk its part is read again: left out by selection, as 0 times an infinity is none
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = fabsf(x[u][i]) == __builtin_inff() ? x[u][i] : x[u][i] * g;
-          v[i] += c < n ? y : 0.f;
-        }
+        for (int i = 0; i < 4; ++i) v[i] += c < n ? x[u][i] * g : 0.f;
       }
     }
   }

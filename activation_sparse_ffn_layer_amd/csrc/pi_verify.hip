@@ -302,7 +302,7 @@ __device__ __forceinline__ void join_bins(const VfDev& p, VfShared& s, const VfB
   v = block_sum<NT>(v, s.red);
   if (threadIdx.x == 0) {
     const double left = s.st.c > 0.0 ? fmax(v.a / v.e - s.st.c * v.q, 0.0) : 1.0;
-    s.again = s.st.z == 0.0 && s.st.c > 0.0 && left < 0x1p20 * fabs(s.rs[s.st.cur] / v.e - 1.0);
+    s.again = s.st.z == 0.0 && s.st.c > 0.0 && left * v.e < 0x1p20 * fabs(s.rs[s.st.cur] - v.e);
     s.st.z = v.e;
     s.st.left = left;
   }
