@@ -61,6 +61,13 @@ def _view(t, name: str, dtype, shape, device: int):
     _refuse(t, name, dtype, shape, device)
 
 
+def _sizes(t, name: str):
+    """The library takes sizes in 32 bits, to which ctypes would cut larger ones without a word."""
+    if max(t.shape) > 0x7FFFFFFF:
+        _bad(f"{name}: sizes are below 2^31, got {tuple(t.shape)}")
+    return t.shape
+
+
 def _common(sa, sb, shape, names: str):
     """Strides that two tensors of this shape share: a stride along one element means nothing."""
     if sa != sb and any(a != b and n != 1 for a, b, n in zip(sa, sb, shape)):
@@ -102,7 +109,7 @@ class KvCache(_Handle):
     def __init__(self, ctx, k: torch.Tensor, v: torch.Tensor):
         if k.dim() != 4 or k.dtype not in (torch.float16, torch.bfloat16):
             _bad("k must be an fp16 or bf16 tensor [pages][page_tokens][heads][head_dim]")
-        pk, sk = _view(k, "k", k.dtype, k.shape, ctx.device)
+        pk, sk = _view(k, "k", k.dtype, _sizes(k, "k"), ctx.device)
         pv, sv = _view(v, "v", k.dtype, k.shape, ctx.device)
         sk = _common(sk, sv, k.shape, "k and v")
         self.ctx, self.k, self.v, self.dtype = ctx, k, v, k.dtype
@@ -118,7 +125,7 @@ def _table(table, B: int, device: int):
         return None, 0, 0
     if table.dim() != 2 or table.shape[0] != B:
         _bad(f"table has shape {tuple(table.shape)}, need [{B}][pages of a sequence]")
-    p, s = _view(table, "table", I32, table.shape, device)
+    p, s = _view(table, "table", I32, _sizes(table, "table"), device)
     return p, s[0], table.shape[1]
 
 
@@ -136,7 +143,7 @@ def kv_append(ctx, cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, tab
     without them) to the positions from ``ctx_len[b]`` on; ``len_out`` gets the new lengths."""
     if k_new.dim() != 4:
         _bad("k_new must be [B][N][heads][head_dim]")
-    dev, (B, N) = ctx.device, k_new.shape[:2]
+    dev, (B, N) = ctx.device, _sizes(k_new, "k_new")[:2]
     pk, pv, s = _new_kv(cache, k_new, v_new, B, N, dev)
     pt, ts, tw = _table(table, B, dev)
     a = AppendArgs(pk, pv, s[0], s[1], s[2], pt, ts, tw, _dense(ctx_len, "ctx_len", I32, (B,), dev),
@@ -168,7 +175,7 @@ def tree_attention(ctx, attn: Attn, q: torch.Tensor, k_new: torch.Tensor, v_new:
     cache = attn.cache
     if q.dim() != 4:
         _bad("q must be [B][N][heads][head_dim]")
-    dev, (B, N) = ctx.device, q.shape[:2]
+    dev, (B, N) = ctx.device, _sizes(q, "q")[:2]
     shape = (B, N, attn.heads, cache.head_dim)
     pq, sq = _view(q, "q", cache.dtype, shape, dev)
     po, so = _view(out, "out", cache.dtype, shape, dev)
@@ -200,7 +207,7 @@ def verify(ctx, ver: Verifier, logits: torch.Tensor, tokens: torch.Tensor, paren
     the draft's probabilities ``q`` (fp32, alike)."""
     if logits.dim() != 3 or logits.dtype not in DTYPE:
         _bad("logits must be a floating-point tensor [B][N][vocab]")
-    dev, (B, N) = ctx.device, logits.shape[:2]
+    dev, (B, N) = ctx.device, _sizes(logits, "logits")[:2]
     shape = (B, N, ver.vocab)
     pl, sl = _view(logits, "logits", logits.dtype, shape, dev)
     pq, sq = (None, (0, 0)) if q is None else _view(q, "q", F32, shape, dev)
@@ -221,7 +228,7 @@ def add_rmsnorm(ctx, x: torch.Tensor, res: Optional[torch.Tensor], w: torch.Tens
     int8 ``q`` [T][d] with one ``scale`` per row, as ``y``, or both."""
     if x.dim() != 2 or x.dtype not in DTYPE:
         _bad("x must be a floating-point tensor [T][d]")
-    dev, shape = ctx.device, x.shape
+    dev, shape = ctx.device, _sizes(x, "x")
     px, sx = _view(x, "x", x.dtype, shape, dev)
     rt = x.dtype if res is None else res.dtype
     if rt not in DTYPE:
@@ -250,7 +257,7 @@ class Linear(_Handle):
                  max_tokens: int = 1):
         if w.dim() != 2:
             _bad("w must be [N][K]")
-        pw, sw = _view(w, "w", I8, w.shape, ctx.device)
+        pw, sw = _view(w, "w", I8, _sizes(w, "w"), ctx.device)
         self.ctx, self.w, self.w_scale, self.bias = ctx, w, w_scale, bias
         self.N, self.K = w.shape
         desc = LinearDesc(self.N, self.K, pw, max(sw[0], self.K) if self.N == 1 else sw[0],
@@ -265,7 +272,7 @@ def linear_q8(ctx, lin: Linear, x: torch.Tensor, x_scale: torch.Tensor, y: torch
     """pi_linear_q8: ``y`` [M][N] = x_scale * w_scale * (x w^T) + bias for int8 ``x`` [M][K]."""
     if x.dim() != 2 or y.dtype not in DTYPE:
         _bad("x must be [M][K] and y a floating-point tensor [M][N]")
-    dev, M = ctx.device, x.shape[0]
+    dev, M = ctx.device, _sizes(x, "x")[0]
     px, sx = _view(x, "x", I8, (M, lin.K), dev)
     py, sy = _view(y, "y", y.dtype, (M, lin.N), dev)
     ps = _dense(x_scale, "x_scale", F32, (M,), dev)

@@ -117,3 +117,24 @@ def test_strides_along_one_element_mean_nothing(cache):
         assert decoder._new_kv(cache, a, b, 3, 1, -1) == (a.data_ptr(), b.data_ptr(), a.stride())
     wide = torch.zeros(3, 1, 2, 128, dtype=F16)[..., :64]
     refused("equal strides", decoder._new_kv, cache, plain, wide, 3, 1, -1)
+
+
+def test_sizes_past_32_bits_are_refused(cache):
+    """Views of one row again and again, 2^32 and a few of them: the library would be told of a few."""
+    many = (1 << 32) + 2
+    here = Ctx()
+    here.device = -1  # the CPU's tensors pass for those of the context's device
+    x = torch.zeros(1, 64, dtype=F16).expand(many, 64)
+    refused("below 2\\^31", pi.add_rmsnorm, here, x, None, torch.ones(64), 1e-5, x)
+    lin = made(pi.Linear, w=None, w_scale=None, bias=None, N=4, K=64)
+    x8, y = torch.zeros(1, 64, dtype=I8).expand(many, 64), torch.zeros(1, 4).expand(many, 4)
+    refused("below 2\\^31", pi.linear_q8, here, lin, x8, torch.ones(1).expand(many), y)
+    refused("below 2\\^31", pi.Linear, here, x8, torch.ones(1).expand(many))
+    k = torch.zeros(1, 1, 2, 64, dtype=F16)
+    refused("below 2\\^31", pi.KvCache, here, k.expand(many, 1, 2, 64), k.expand(many, 1, 2, 64))
+    refused("below 2\\^31", pi.kv_append, here, cache, k.expand(1, many, 2, 64), k.expand(1, many, 2, 64), None,
+            torch.zeros(1, dtype=I32))
+    attn, q = made(pi.Attn, cache=cache, heads=2), k.expand(many, 1, 2, 64)
+    refused("below 2\\^31", pi.tree_attention, here, attn, q, q, q, None, None, torch.zeros(1, dtype=I32).expand(many), q)
+    ver, z, i = made(pi.Verifier, vocab=1), torch.zeros(1, 1, 1).expand(many, 1, 1), torch.zeros(1, 1, dtype=I32).expand(many, 1)
+    refused("below 2\\^31", pi.verify, here, ver, z, i, i, z[..., 0], z[:, 0, 0], i, i, i[:, 0])
