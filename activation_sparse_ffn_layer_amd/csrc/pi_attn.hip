@@ -203,6 +203,9 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   const int hk = pair % a.HK, slot = pair / a.HK;
   Chunk ch;
   if (!find_chunk<KT>(a, slot, &ch)) return;
+  // the same on every lane, which the shuffles that found it hide: kept in scalar registers
+  ch = Chunk{__builtin_amdgcn_readfirstlane(ch.b), __builtin_amdgcn_readfirstlane(ch.t0), __builtin_amdgcn_readfirstlane(ch.t1),
+             __builtin_amdgcn_readfirstlane(ch.count), __builtin_amdgcn_readfirstlane(ch.first)};
   if (threadIdx.x == 0) s_odd = 0;
   __syncthreads();
   const int b = ch.b;
