@@ -390,13 +390,17 @@ int split_count(int cus, int tiles, int K) {
 
 // Up to 16 tokens. Each workgroup of k_q8_rows reads all of x, which costs 4.4 us per 10^9 of M N K (the
 // same at all six shapes measured); tiles read it once for 128 rows, but join their ranges' sums, 2 to
-// 5 us. Rows against tiles, us: K = 4096, N = 12288: 12.1 / 17.1 at one token, 15.4 / 17.8 at 16;
-// K = 8192, N = 10240: 20.6 / 21.7 at 2, 22.2 / 22.0 at 6, 26.9 / 22.9 at 16; K = 4096, N = 32000:
-// 29.7 / 30.5 at 6, 34.2 / 31.2 at 12; K = 8192, N = 28672: 46.5 / 48.0 at 3, 51.9 / 49.0 at 8. Few rows
-// of great length leave most CUs without any: K = 16384, N = 1024: 12.8 / 11.4 at 2, 17.2 / 12.2 at 16,
-// but K = 8192, N = 1024: 8.8 / 9.3 at 8. One token has no use for tiles, nor their scratch.
+// 5 us, most where the weight is below 64 MB and a range is a few steps. Rows against tiles, us: K = 4096,
+// N = 12288: 12.1 / 17.1 at one token, 15.4 / 17.8 at 16; K = 8192, N = 4096: 10.8 / 14.5 at 16; N = 10240:
+// 20.6 / 21.7 at 2, 22.2 / 22.0 at 6, 23.1 / 22.2 at 8, 26.9 / 22.9 at 16; K = 4096, N = 32000: 29.7 / 30.5
+// at 6, 34.2 / 31.2 at 12; K = 8192, N = 28672: 46.5 / 48.0 at 3, 51.9 / 49.0 at 8. Few rows of great length
+// leave most CUs without any: K = 16384, N = 1024: 12.8 / 11.4 at 2, 17.2 / 12.2 at 16, but K = 8192: 8.8 /
+// 9.3 at 8. One token has no use for tiles, nor their scratch.
 bool by_rows(int M, int N, int K) {
-  return M == 1 || (M <= 16 && (long long)M * N * K < 850000000 && K <= 8ll * N);
+  if (M == 1) return true;
+  if (M > 16 || K > 8ll * N) return false;
+  const long long weights = (long long)N * K;
+  return weights < (1 << 26) || (M * K < 65536 && M * weights < 850000000);
 }
 
 template <typename T>
