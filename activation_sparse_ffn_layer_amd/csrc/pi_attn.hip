@@ -15,9 +15,9 @@
 //
 // Many rows are bound by the products and the weights' exponentials, which take the SIMDs nearly in
 // turn (47% and 48% of the busy cycles) at a clock that falls to 1.75 GHz: 64 nodes of 64 heads (8
-// key heads) over 65536 positions of 128, 137 GFLOP, 155 to 185 us and 10 us for the join. 26 nodes
-// of 4 sequences (25 000 positions, 108 MB): 41 us and 10 us. One node of 32 heads over 512
-// positions is a chain of latencies: 10 us and 4 us; joining in the last workgroup to arrive
+// key heads) over 65536 positions of 128, 137 GFLOP, 160 to 210 us and 10 us for the join. 26 nodes
+// of 4 sequences (25 000 positions, 108 MB): 43 us and 10 us. One node of 32 heads over 512
+// positions is a chain of latencies: 9.6 us and 4.6 us; joining in the last workgroup to arrive
 // instead took 22 us (its release fences). Four waves of 32 rows (two workgroups per CU) were
 // slower than eight, 62 against 54 us and 227 against 190; so was working a block's scores out
 // under the weights of the one before, 60 and 211.

@@ -2,8 +2,8 @@
 //
 // r = round(x + res), y = r / sqrt(mean(r^2) + eps) * w, scale = max|y| / 127, q = round(y / scale).
 // Bound by memory: a row is read once, kept in registers between its three steps (sum of
-// squares, maximum, output) and written once. 4096 rows of 8192 in fp16, 235 MB: 46 us, 5.1 TB/s,
-// the rate of a plain copy; 8 rows of 4096: 4.2 us, the latency of a load, two sums over the
+// squares, maximum, output) and written once. 4096 rows of 8192 in fp16, 235 MB: 47 to 49 us, 4.9 TB/s,
+// the rate of a plain copy; 8 rows of 4096: 4.4 us, the latency of a load, two sums over the
 // workgroup and a store. One workgroup per row, 8 columns per thread and
 // step; the two sums over the row go through LDS.
 #include "pi_host.hpp"

@@ -23,8 +23,8 @@
 //                   once where the sequence is done).
 //   k_verify_end    a workgroup per sequence does whatever is left and draws the next token: the
 //                   chunk by the chunks' weights, then the token inside it.
-// The passes and the end are chains of dependent loads, sums over a workgroup and the walk: 15, 7
-// and 12 us at 16 trees of 32 nodes, 8, 3 and 10 at one chain of 5.
+// The passes and the end are chains of dependent loads, sums over a workgroup and the walk: 14, 7
+// and 12 us at 16 trees of 32 nodes, 8, 3 and 8 at one chain of 5.
 #include <algorithm>
 #include <new>
 
