@@ -654,13 +654,18 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
   __builtin_memcpy(__builtin_assume_aligned(o, 8), &w, 8);
 }
 
-// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences).
+// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences). Up to heads of
+// 128 as few waves as the rows need. Above, a wave's query and output fill the registers, and only what
+// eight waves share of a tile's loads leaves room for them: with one, two and four waves 348, 84 and 89
+// registers were spilled, with eight 32, and eight are the fastest also where most of them have no rows.
+// 8191 positions, 4 key heads of 256: 4 rows each 32 us (one wave: 67 to 77), 4 sequences of 48 rows 60
+// (two: 270), 128 rows 42 (four: 67 to 71), 4 sequences of 104 rows 68 (four: 109).
 struct AttnPlan {
   int wq, row_tiles, slots;
 };
-AttnPlan attn_plan(int cus, int HK, int rows, int B) {
+AttnPlan attn_plan(int cus, int HK, int rows, int B, int DP) {
   AttnPlan p;
-  p.wq = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
+  p.wq = DP > 128 ? 8 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
   p.row_tiles = (rows + 32 * p.wq - 1) / (32 * p.wq);
   const int wgs = p.wq == 8 ? cus : 2 * cus;  // workgroups the chip holds at once
   p.slots = std::max(B, wgs / (HK * p.row_tiles));
@@ -683,12 +688,15 @@ pi_status launch_attn_t(pi_ctx* c, const AttnDev& a) {
 
 template <typename T, int DP>
 pi_status launch_attn_d(pi_ctx* c, const AttnDev& a, int wq) {
-  constexpr int KB = DP <= 128 ? 2 : 1;
-  switch (wq) {
-    case 1: return launch_attn_t<T, DP, 1, 4, 1>(c, a);
-    case 2: return launch_attn_t<T, DP, 2, 2, 1>(c, a);
-    case 4: return launch_attn_t<T, DP, 4, 1, KB>(c, a);
-    default: return launch_attn_t<T, DP, 8, 1, KB>(c, a);
+  if constexpr (DP > 128) {
+    return launch_attn_t<T, DP, 8, 1, 1>(c, a);
+  } else {
+    switch (wq) {
+      case 1: return launch_attn_t<T, DP, 1, 4, 1>(c, a);
+      case 2: return launch_attn_t<T, DP, 2, 2, 1>(c, a);
+      case 4: return launch_attn_t<T, DP, 4, 1, 2>(c, a);
+      default: return launch_attn_t<T, DP, 8, 1, 2>(c, a);
+    }
   }
 }
 
@@ -723,7 +731,7 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
   // scratch of the largest call: rows (all heads, all slots) of any number of nodes and sequences
   size_t rows = 0;
   for (int n = 1; n <= max_nodes; ++n) {
-    const AttnPlan p = attn_plan(ctx->cus, HK, n * G, max_batch);
+    const AttnPlan p = attn_plan(ctx->cus, HK, n * G, max_batch, DP);
     rows = std::max(rows, (size_t)p.slots * HK * n * G);
   }
   PI_HIP(ctx, hipSetDevice(ctx->device));
@@ -778,7 +786,7 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
   if (reinterpret_cast<uintptr_t>(a.tree) & 7u) return fail(ctx, PI_ERR_INVALID, "tree is not 8-byte aligned");
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const int HK = kv->desc.heads, G = attn->heads / HK;
-  const AttnPlan p = attn_plan(ctx->cus, HK, a.N * G, a.B);
+  const AttnPlan p = attn_plan(ctx->cus, HK, a.N * G, a.B, padded_dim(kv->desc.head_dim));
   KvDev c = kv_dev(kv, a.table, a.table_stride, a.table_width);
   if (a.table == nullptr) {
     c.table = attn->self;
