@@ -14,13 +14,15 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from .decoder import (Attn, KvCache, Linear, Verifier, add_rmsnorm, kv_append, linear_q8, tree_attention, verify)
+from .decoder import (Attn, KvCache, KvCache4, Linear, PromptAttn, Verifier, add_rmsnorm, kv_append, kv_read, linear_q8,
+                      prompt_attention, qk_norm_rope, tree_attention, verify)
 from ._lib import ACT, KERNEL_CLASSES, MASK_MODE, PI_OK, WTYPE, FfnDesc, PiError, StackDump, _ptr, lib
 
 __all__ = ["Context", "Ffn", "PiError", "predict", "sparse_ffn", "layer", "layer_noalloc", "q4_dequant", "compact", "glue", "stack_run",
            "stack_run_dump", "stack_profile", "KERNEL_CLASSES",
-           "hot_first_order", "permute_rows", "lib", "KvCache", "Attn", "Verifier", "Linear", "kv_append",
-           "tree_attention", "verify", "add_rmsnorm", "linear_q8"]
+           "hot_first_order", "permute_rows", "lib", "KvCache", "KvCache4", "Attn", "PromptAttn", "Verifier", "Linear",
+           "kv_append", "kv_read", "tree_attention", "prompt_attention", "qk_norm_rope", "verify", "add_rmsnorm",
+           "linear_q8"]
 
 
 class Context:

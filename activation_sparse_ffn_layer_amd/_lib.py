@@ -78,6 +78,36 @@ class LinearDesc(ctypes.Structure):
                 ("bias", c_void_p), ("max_tokens", c_int32)]
 
 
+class Kv4Desc(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("heads", c_int32), ("head_dim", c_int32), ("pages", c_int32),
+                ("page_tokens", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("page_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64),
+                ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("scale_page_stride", c_int64), ("scale_token_stride", c_int64), ("scale_head_stride", c_int64)]
+
+
+class ReadArgs(ctypes.Structure):
+    _fields_ = [("table", c_void_p), ("table_stride", c_int64), ("table_width", c_int32), ("ctx_len", c_void_p),
+                ("start", c_void_p), ("cu", c_void_p), ("k_out", c_void_p), ("v_out", c_void_p),
+                ("out_row", c_int64), ("out_head", c_int64), ("B", c_int32), ("rows", c_int32)]
+
+
+class PromptArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("q_row", c_int64), ("q_head", c_int64), ("k", c_void_p),
+                ("k_row", c_int64), ("k_head", c_int64), ("v", c_void_p), ("v_row", c_int64), ("v_head", c_int64),
+                ("out", c_void_p), ("out_row", c_int64), ("out_head", c_int64), ("cu_q", c_void_p), ("cu_k", c_void_p), ("B", c_int32), ("q_rows", c_int32),
+                ("k_rows", c_int32)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("q_row", c_int64), ("q_head", c_int64), ("k_row", c_int64),
+                ("k_head", c_int64), ("q_out", c_void_p), ("k_out", c_void_p), ("q_out_row", c_int64),
+                ("q_out_head", c_int64), ("k_out_row", c_int64), ("k_out_head", c_int64), ("x_dtype", c_int32),
+                ("y_dtype", c_int32), ("q_w", c_void_p), ("k_w", c_void_p), ("eps", c_float), ("pos", c_void_p),
+                ("inv_freq", c_void_p), ("rot", c_int32), ("interleaved", c_int32), ("T", c_int32),
+                ("heads", c_int32), ("kv_heads", c_int32), ("head_dim", c_int32)]
+
+
 _SIGS = {
     "pi_abi_version": (c_int32, []),
     "pi_status_str": (ctypes.c_char_p, [c_int32]),
@@ -106,6 +136,12 @@ _SIGS = {
     "pi_permute_rows": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64]),
     "pi_kv_create": (c_int32, [c_void_p, POINTER(KvDesc), POINTER(c_void_p)]),
     "pi_kv_destroy": (None, [c_void_p]),
+    "pi_kv4_create": (c_int32, [c_void_p, POINTER(Kv4Desc), POINTER(c_void_p)]),
+    "pi_kv_read": (c_int32, [c_void_p, c_void_p, POINTER(ReadArgs)]),
+    "pi_prompt_create": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_float, POINTER(c_void_p)]),
+    "pi_prompt_destroy": (None, [c_void_p]),
+    "pi_prompt_attention": (c_int32, [c_void_p, c_void_p, POINTER(PromptArgs)]),
+    "pi_qk_norm_rope": (c_int32, [c_void_p, POINTER(RopeArgs)]),
     "pi_kv_append": (c_int32, [c_void_p, c_void_p, POINTER(AppendArgs)]),
     "pi_attn_create": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_float, POINTER(c_void_p)]),
     "pi_attn_destroy": (None, [c_void_p]),

@@ -10,8 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpi.so")
-SOURCES = [os.path.join(CSRC, n) for n in ("pi_lib.hip", "pi_attn.hip", "pi_kv.hip", "pi_linear.hip", "pi_norm.hip",
-                                           "pi_verify.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("pi_lib.hip", "pi_attn.hip", "pi_attn4.hip", "pi_kv.hip", "pi_linear.hip",
+                                           "pi_norm.hip", "pi_prompt.hip", "pi_rope.hip", "pi_verify.hip")]
 
 
 def hipcc() -> str:

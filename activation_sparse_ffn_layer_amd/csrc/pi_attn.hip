@@ -24,146 +24,12 @@
 #include <algorithm>
 #include <new>
 
-#include "pi_kv.hpp"
+#include "pi_attn.hpp"
 
 using namespace pi;
 
-struct pi_attn {
-  pi_ctx* ctx;
-  pi_kv kv;         // a copy: the cache's handle may be destroyed before this one
-  int heads, max_batch, max_nodes;
-  float scale;
-  uint8_t* ws;
-  float* part;      // [slots][kv heads][rows][DP]
-  float* ml;        // [slots][kv heads][rows][2]: maximum (log2 domain) and sum
-  int32_t* self;    // 0, 1, ..: the page table of calls without one
-};
-
 namespace {
 
-struct AttnDev {
-  KvDev c;
-  const uint8_t *q, *kn, *vn;
-  uint8_t* out;
-  const uint64_t* tree;
-  const int32_t* ctx_len;
-  float *part, *ml;
-  long long q_batch, q_node, q_head, kv_batch, kv_node, kv_head, out_batch, out_node, out_head;
-  int B, N, H, HK, G, D, R;  // R = N * G query rows of a key/value head
-  int slots, row_tiles;
-  float scale2;  // scale * log2(e)
-};
-
-template <typename T> struct Mm;
-template <> struct Mm<half_t> {
-  typedef half8_t v8;
-  // weights are carried times 2^14 (at most 16384), so that fp16 keeps its 11 bits down to 2^-28
-  // of the largest; below, a long cache's many small weights would round away together
-  static constexpr float SHIFT = 14.f;
-  static constexpr uint32_t EXP = 0x7C00u;
-  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
-  }
-};
-template <> struct Mm<bf16_t> {
-  typedef bf8_t v8;
-  static constexpr float SHIFT = 0.f;
-  static constexpr uint32_t EXP = 0x7F80u;
-  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-  }
-};
-
-__device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
-
-// The other half's value of v (lane ^ 32).
-__device__ __forceinline__ float swap_max(float v) {
-  const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-  return fmaxf(u2f(p[0]), u2f(p[1]));
-}
-__device__ __forceinline__ float swap_add(float v) {
-  const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-  return u2f(p[0]) + u2f(p[1]);
-}
-
-// Tiles of KT keys that a sequence's positions and nodes take. Positions go up to 2^31 - 65 and a tile
-// or its successors may end beyond 2^31: sums of them are unsigned, and the kernels go by a tile's
-// place relative to the sequence's end, which is small where it matters.
-template <int KT>
-__device__ __forceinline__ int key_tiles(const AttnDev& a, int b) {
-  return (int)(((uint32_t)kv_len(a.c, a.ctx_len, b) + (uint32_t)(a.N + KT - 1)) / (uint32_t)KT);
-}
-template <int KT>
-__device__ __forceinline__ int tile_from_end(int tile, int len) {
-  return (int)((uint32_t)tile * (uint32_t)KT - (uint32_t)len);
-}
-// A sum over all sequences of what each lane adds up: a lane's stops at 2^25, above any number of slots
-// that it is compared with, so that 64 of them stay below 2^32.
-__device__ __forceinline__ uint32_t lane_tiles(uint32_t n, uint32_t more) { return min(n + more, 1u << 25); }
-__device__ __forceinline__ uint32_t sum_tiles(uint32_t n) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s, WAVE);
-  return n;
-}
-
-// Where chunk `slot` lies: sequence b, its tiles [t0, t1), its number of chunks and the first
-// one's slot; false past the last chunk. Chunks are `c` tiles long, the least c that needs no
-// more than `slots` of them in all (slots >= B). Every wave works it out for itself.
-struct Chunk {
-  int b, t0, t1, count, first;
-};
-template <int KT>
-__device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o) {
-  const int lane = threadIdx.x % WAVE;
-  auto tiles = [&](int b) { return b < a.B ? key_tiles<KT>(a, b) : 0; };
-  if (a.B == 1) {
-    const int t = tiles(0), c = (t + a.slots - 1) / a.slots;
-    *o = Chunk{0, slot * c, min(t, slot * c + c), (t + c - 1) / c, 0};
-    return o->t0 < t;
-  }
-  const int mine = tiles(lane);  // the sequence of this lane; more than 64 are read again
-  auto sum = [&](int c) {
-    uint32_t n = lane_tiles(lane < a.B ? (mine + c - 1) / c : 0, 0);
-    for (int b = lane + WAVE; b < a.B; b += WAVE) n = lane_tiles(n, (tiles(b) + c - 1) / c);
-    return sum_tiles(n);
-  };
-  const uint32_t slots = (uint32_t)a.slots;
-  int c = max(1, (int)((sum(1) + slots - 1) / slots));
-  while (c > 1 && sum(c) > slots) c += max(1, c >> 5);
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += WAVE) {
-    const int tl = b0 == 0 ? mine : tiles(b0 + lane);
-    const int n = (tl + c - 1) / c;
-    int incl = n;
-#pragma unroll
-    for (int s = 1; s < WAVE; s <<= 1) {
-      const int t = __shfl_up(incl, s, WAVE);
-      if (lane >= s) incl += t;
-    }
-    const uint64_t hit = __ballot(before + incl > slot);
-    if (hit != 0) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int first = before + __shfl(incl - n, l, WAVE);
-      const int tb = __shfl(tl, l, WAVE);
-      o->b = b0 + l;
-      o->first = first;
-      o->count = __shfl(n, l, WAVE);
-      o->t0 = (slot - first) * c;
-      o->t1 = min(tb, o->t0 + c);
-      return true;
-    }
-    before += __shfl(incl, WAVE - 1, WAVE);
-  }
-  return false;
-}
-
-__device__ u32x4 attn_zero;  // zeros, never written
-
-// LDS of a workgroup: keys, then values, of one tile (two where tiles are shared by waves). A
-// row's pitch spreads what is read at once over the 64 banks: 16 rows of 16 bytes of K, and of V,
-// by its transposing reads, 4 rows of 64 bytes.
-template <int DP> constexpr int k_pitch() { return DP * 2 + 16; }
-template <int DP> constexpr int v_pitch() { return DP * 2 % 128 == 0 ? DP * 2 + 64 : DP * 2; }
 template <int DP, int WQ, int WK, int KB>
 constexpr size_t attn_lds() {
   const size_t kt = 32 * KB * WK;
@@ -580,89 +446,12 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
   }
 }
 
-// Bound by memory, the partial results' bytes (27 MB at 6656 rows in some 13 chunks: 10 us).
-// out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over a sequence's chunks s, one wave per
-// query row, 4 columns per lane; rows of sequences of one chunk are done already.
-template <typename T, int DP, int KT>
-__global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
-  const int lane = threadIdx.x % WAVE;
-  // (b, hk, r) of this wave
-  const int id = blockIdx.x * NWAVES + threadIdx.x / WAVE;
-  if (id >= rows) return;
-  const int r = id % a.R, hk = id / a.R % a.HK, b = id / a.R / a.HK;
-  // the first slot of sequence b: the chunks before it
-  auto tiles = [&](int i) { return i < a.B ? key_tiles<KT>(a, i) : 0; };
-  auto sum = [&](int c, int end) {
-    uint32_t n = 0;
-    for (int i = lane; i < end; i += WAVE) n = lane_tiles(n, (tiles(i) + c - 1) / c);
-    return sum_tiles(n);
-  };
-  const uint32_t slots = (uint32_t)a.slots;
-  int c = max(1, (int)((sum(1, a.B) + slots - 1) / slots));
-  while (c > 1 && sum(c, a.B) > slots) c += max(1, c >> 5);
-  const int first = (int)sum(c, b), count = (tiles(b) + c - 1) / c;
-  if (count == 1) return;
-  const long long at0 = ((long long)first * a.HK + hk) * a.R + r, next = (long long)a.HK * a.R;
-  float m = -__builtin_inff();
-  for (int s = lane; s < count; s += WAVE) m = fmaxf(m, a.ml[2 * (at0 + s * next)]);
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, WAVE));
-  const float base = m == -__builtin_inff() ? 0.f : m;
-  // Up to 128 columns the wave's halves take every other chunk.
-  constexpr int HALVES = DP <= 128 ? 2 : 1;
-  const int mine = HALVES == 2 ? lane >> 5 : 0, d = 4 * (HALVES == 2 ? lane & 31 : lane);
-  const float* part = a.part + at0 * DP + min(d, DP - 4);
-  f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int s0 = 0; s0 < count; s0 += WAVE) {
-    // a lane's chunk of these 64: its factor and its part of the sum
-    const bool in = s0 + lane < count;
-    const long long at = at0 + (in ? s0 + lane : 0) * next;
-    // not 0 for a chunk of this sequence: an infinity that its row sees stays one, whatever it weighs
-    const float f = in ? fmaxf(__builtin_amdgcn_exp2f(a.ml[2 * at] - base), 1.4e-45f) : 0.f;
-    l += in ? a.ml[2 * at + 1] * f : 0.f;
-    const int n = min(WAVE, count - s0);
-    for (int s = 0; s < n; s += 8) {
-      constexpr int U = 8 / HALVES;
-      f32x4 x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const f32x4*>(part + (s0 + min(s + HALVES * u + mine, n - 1)) * next * DP);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = s + HALVES * u + mine;
-        // the halves ask different lanes: what is shuffled must not depend on the asking lane's c
-        const float g = __shfl(f, min(c, n - 1), WAVE);
-        // past the last chunk its part is read again: left out by selection, as 0 times an infinity is none
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += c < n ? x[u][i] * g : 0.f;
-      }
-    }
-  }
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s, WAVE);
-  if constexpr (HALVES == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = swap_add(v[i]);
-  }
-  if (HALVES == 2 && lane >= 32) return;
-  if (d >= a.D) return;
-  T* o = reinterpret_cast<T*>(a.out) + (long long)b * a.out_batch + (long long)(r / a.G) * a.out_node +
-         (long long)(hk * a.G + r % a.G) * a.out_head + d;
-  struct __attribute__((aligned(8))) { T e[4]; } w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w.e[i] = (T)(l == 0.f ? 0.f : v[i] / l);
-  __builtin_memcpy(__builtin_assume_aligned(o, 8), &w, 8);
-}
-
-// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences). Up to heads of
+// The plan of a call (pi_attn.hpp). Up to heads of
 // 128 as few waves as the rows need. Above, a wave's query and output fill the registers, and only what
 // eight waves share of a tile's loads leaves room for them: with one, two and four waves 348, 84 and 89
 // registers were spilled, with eight 32, and eight are the fastest also where most of them have no rows.
 // 8191 positions, 4 key heads of 256: 4 rows each 32 us (one wave: 67 to 77), 4 sequences of 48 rows 60
 // (two: 270), 128 rows 42 (four: 67 to 71), 4 sequences of 104 rows 68 (four: 109).
-struct AttnPlan {
-  int wq, row_tiles, slots;
-};
 AttnPlan attn_plan(int cus, int HK, int rows, int B, int DP) {
   AttnPlan p;
   p.wq = DP > 128 ? 8 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
@@ -671,8 +460,6 @@ AttnPlan attn_plan(int cus, int HK, int rows, int B, int DP) {
   p.slots = std::max(B, wgs / (HK * p.row_tiles));
   return p;
 }
-constexpr int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
-
 template <typename T, int DP, int WQ, int WK, int KB>
 pi_status launch_attn_t(pi_ctx* c, const AttnDev& a) {
   constexpr size_t lds = attn_lds<DP, WQ, WK, KB>();
@@ -725,13 +512,14 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
   if (max_batch < 1 || max_nodes < 1) return fail(ctx, PI_ERR_INVALID, "bad limits: %d sequences, %d nodes", max_batch, max_nodes);
   if (max_nodes > 64) return fail(ctx, PI_ERR_UNSUPPORTED, "%d nodes: a tree has at most 64", max_nodes);
   if (!(scale > 0.f) || scale > 3e38f) return fail(ctx, PI_ERR_INVALID, "scale must be finite and above 0");
-  const int HK = kv->desc.heads, G = heads / HK, DP = padded_dim(kv->desc.head_dim);
+  const int HK = kv->desc.heads, G = heads / HK;
+  const int DP = kv->q4 ? padded_dim4(kv->desc.head_dim) : padded_dim(kv->desc.head_dim);
   if ((int64_t)max_batch * max_nodes * heads >= (1ll << 31) / 64)
     return fail(ctx, PI_ERR_UNSUPPORTED, "%d sequences of %d nodes and %d heads are too many", max_batch, max_nodes, heads);
   // scratch of the largest call: rows (all heads, all slots) of any number of nodes and sequences
   size_t rows = 0;
   for (int n = 1; n <= max_nodes; ++n) {
-    const AttnPlan p = attn_plan(ctx->cus, HK, n * G, max_batch, DP);
+    const AttnPlan p = (kv->q4 ? attn4_plan : attn_plan)(ctx->cus, HK, n * G, max_batch, DP);
     rows = std::max(rows, (size_t)p.slots * HK * n * G);
   }
   PI_HIP(ctx, hipSetDevice(ctx->device));
@@ -786,7 +574,8 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
   if (reinterpret_cast<uintptr_t>(a.tree) & 7u) return fail(ctx, PI_ERR_INVALID, "tree is not 8-byte aligned");
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const int HK = kv->desc.heads, G = attn->heads / HK;
-  const AttnPlan p = attn_plan(ctx->cus, HK, a.N * G, a.B, padded_dim(kv->desc.head_dim));
+  const int D = kv->desc.head_dim;
+  const AttnPlan p = kv->q4 ? attn4_plan(ctx->cus, HK, a.N * G, a.B, padded_dim4(D)) : attn_plan(ctx->cus, HK, a.N * G, a.B, padded_dim(D));
   KvDev c = kv_dev(kv, a.table, a.table_stride, a.table_width);
   if (a.table == nullptr) {
     c.table = attn->self;
@@ -797,6 +586,7 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
                   static_cast<uint8_t*>(a.out), a.tree, a.ctx_len, attn->part, attn->ml, a.q_batch, a.q_node, a.q_head,
                   a.kv_batch, a.kv_node, a.kv_head, a.out_batch, a.out_node, a.out_head, a.B, a.N, attn->heads, HK, G,
                   kv->desc.head_dim, a.N * G, p.slots, p.row_tiles, attn->scale * 1.4426950408889634f};
+  if (kv->q4) return launch_attn4(ctx, d, kv4_dev(kv), p.wq, kv->desc.dtype == PI_T_F16);
   return kv->desc.dtype == PI_T_F16 ? launch_attn<half_t>(ctx, d, p.wq) : launch_attn<bf16_t>(ctx, d, p.wq);
 }
 

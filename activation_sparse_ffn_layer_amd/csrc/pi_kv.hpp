@@ -4,8 +4,11 @@
 #include "pi_types.hpp"
 
 struct pi_kv {
-  pi_kv_desc desc;
+  pi_kv_desc desc;   // of a 4-bit cache: the codes, strides in bytes
   pi_ctx* ctx;
+  bool q4 = false;   // a 4-bit cache, with these scales
+  uint16_t *k_scale = nullptr, *v_scale = nullptr;
+  int64_t scale_page = 0, scale_token = 0, scale_head = 0;
 };
 
 namespace pi {
@@ -69,6 +72,26 @@ inline KvDev kv_dev(const pi_kv* kv, const int32_t* table, int64_t table_stride,
   const pi_kv_desc& d = kv->desc;
   return KvDev{d.k, d.v, d.page_stride, d.token_stride, d.head_stride, table, table_stride,
                page_div((uint32_t)d.page_tokens), d.pages, table != nullptr ? width * d.page_tokens : d.page_tokens};
+}
+
+// The scales of a 4-bit cache; its codes are KvDev's k and v, with strides in bytes.
+struct Kv4Dev {
+  uint16_t *ks, *vs;
+  long long page, token, head;
+};
+inline Kv4Dev kv4_dev(const pi_kv* kv) { return Kv4Dev{kv->k_scale, kv->v_scale, kv->scale_page, kv->scale_token, kv->scale_head}; }
+
+// Four code bytes of a block (byte j: element j | element j + 16 << 4) as 8 fp16 values (code - 8) in
+// pairs: out[0] elements j, j+2; out[1] j+1, j+3; out[2] 16+j, 16+j+2; out[3] 16+j+1, 16+j+3. A
+// nibble in the low mantissa bits of 1024 stands for 1024 + code, four bits further up for 1024 + 16 code.
+__device__ __forceinline__ void q4_pairs(uint32_t w, half2_t (&out)[4]) {
+  const uint32_t u = w >> 8;
+  const half2_t lo = (half2_t){(half_t)1032.f, (half_t)1032.f}, sixteenth = (half2_t){(half_t)0.0625f, (half_t)0.0625f},
+                hi = (half2_t){(half_t)-72.f, (half_t)-72.f};
+  out[0] = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u) - lo;
+  out[1] = __builtin_bit_cast(half2_t, (u & 0x000F000Fu) | 0x64006400u) - lo;
+  out[2] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u), sixteenth, hi);
+  out[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (u & 0x00F000F0u) | 0x64006400u), sixteenth, hi);
 }
 
 // Strides of a [B][N][heads][D] tensor of 16-bit elements whose rows are 16-byte aligned.

@@ -1,7 +1,8 @@
 """The decoder operators around the sparse FFN, over the C ABI of include/pi.h.
 
-:class:`KvCache`, :class:`Attn`, :class:`Verifier` and :class:`Linear` wrap the handles;
-:func:`kv_append`, :func:`tree_attention`, :func:`verify`, :func:`add_rmsnorm` and
+:class:`KvCache`, :class:`KvCache4`, :class:`Attn`, :class:`PromptAttn`, :class:`Verifier` and
+:class:`Linear` wrap the handles; :func:`kv_append`, :func:`kv_read`, :func:`tree_attention`,
+:func:`prompt_attention`, :func:`qk_norm_rope`, :func:`verify`, :func:`add_rmsnorm` and
 :func:`linear_q8` enqueue the operators on the context's stream. Tensors may be views as long
 as their last axis is contiguous. Shapes, types and devices are checked here (:class:`PiError`
 with the status of an invalid argument), everything else in the library.
@@ -14,10 +15,10 @@ from typing import Optional
 
 import torch
 
-from ._lib import (DTYPE, PI_ERR_INVALID, AppendArgs, AttnArgs, KvDesc, LinearDesc, NormArgs, PiError, VerifyArgs,
-                   lib)
+from ._lib import (DTYPE, PI_ERR_INVALID, AppendArgs, AttnArgs, Kv4Desc, KvDesc, LinearDesc, NormArgs, PiError, PromptArgs,
+                   ReadArgs, RopeArgs, VerifyArgs, lib)
 
-I8, I32, I64, F32 = torch.int8, torch.int32, torch.int64, torch.float32
+I8, U8, I32, I64, F16, F32 = torch.int8, torch.uint8, torch.int32, torch.int64, torch.float16, torch.float32
 
 
 def _bad(msg: str):
@@ -119,6 +120,43 @@ class KvCache(_Handle):
         ctx.check(lib().pi_kv_create(ctx.handle, ctypes.byref(desc), ctypes.byref(h)))
         self.handle = h
 
+    def tensors(self):
+        return self.k, self.v
+
+
+class KvCache4(_Handle):
+    """A pi_kv of pi_kv4_create: a layer's key/value cache in 4 bits over borrowed tensors: codes ``k`` and ``v``
+    uint8 [pages][page_tokens][heads][head_dim/2], ``k_scale`` and ``v_scale`` fp16
+    [pages][page_tokens][heads][head_dim/32] (each pair of equal strides). ``dtype`` is the type of the tokens
+    appended, read and attended with. It is taken wherever a :class:`KvCache` is."""
+
+    _destroy = "pi_kv_destroy"
+
+    def __init__(self, ctx, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 dtype: torch.dtype = torch.float16):
+        if dtype not in (torch.float16, torch.bfloat16):
+            _bad(f"dtype is {dtype}, need fp16 or bf16")
+        if k.dim() != 4 or k.dtype is not U8 or k.shape[3] % 16:
+            _bad("k must be a uint8 tensor [pages][page_tokens][heads][head_dim/2], head_dim a multiple of 32")
+        pk, sk = _view(k, "k", U8, _sizes(k, "k"), ctx.device)
+        pv, sv = _view(v, "v", U8, k.shape, ctx.device)
+        sk = _common(sk, sv, k.shape, "k and v")
+        shape = (*k.shape[:3], k.shape[3] // 16)
+        pks, ss = _view(k_scale, "k_scale", F16, shape, ctx.device)
+        pvs, svs = _view(v_scale, "v_scale", F16, shape, ctx.device)
+        ss = _common(ss, svs, shape, "k_scale and v_scale")
+        self.ctx, self.k, self.v, self.k_scale, self.v_scale, self.dtype = ctx, k, v, k_scale, v_scale, dtype
+        self.pages, self.page_tokens, self.heads = k.shape[:3]
+        self.head_dim = 2 * k.shape[3]
+        desc = Kv4Desc(DTYPE[dtype], self.heads, self.head_dim, self.pages, self.page_tokens, pk, pv, sk[0], sk[1], sk[2],
+                       pks, pvs, ss[0], ss[1], ss[2])
+        h = c_void_p()
+        ctx.check(lib().pi_kv4_create(ctx.handle, ctypes.byref(desc), ctypes.byref(h)))
+        self.handle = h
+
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
 
 def _table(table, B: int, device: int):
     if table is None:
@@ -149,12 +187,30 @@ def kv_append(ctx, cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, tab
     a = AppendArgs(pk, pv, s[0], s[1], s[2], pt, ts, tw, _dense(ctx_len, "ctx_len", I32, (B,), dev),
                    _opt(nodes, "nodes", I32, (B, N), dev), _opt(n, "n", I32, (B,), dev),
                    _opt(len_out, "len_out", I32, (B,), dev), B, N)
-    _borrow(ctx, k_new, v_new, table, ctx_len, len_out, nodes, n, cache.k, cache.v)
+    _borrow(ctx, k_new, v_new, table, ctx_len, len_out, nodes, n, *cache.tensors())
     ctx.check(lib().pi_kv_append(ctx.handle, cache.handle, ctypes.byref(a)))
 
 
+def kv_read(ctx, cache, table: Optional[torch.Tensor], ctx_len: torch.Tensor, cu: torch.Tensor, k_out: torch.Tensor,
+            v_out: torch.Tensor, start: Optional[torch.Tensor] = None):
+    """pi_kv_read: rows ``cu[b]`` to ``cu[b + 1]`` of ``k_out`` and ``v_out`` [rows][heads][head_dim] from sequence
+    b's positions from ``start[b]`` (0 without it) on; rows beyond its ``ctx_len`` stay as they are."""
+    if k_out.dim() != 3 or ctx_len.dim() != 1:
+        _bad("k_out must be [rows][heads][head_dim] and ctx_len [B]")
+    dev, rows, B = ctx.device, _sizes(k_out, "k_out")[0], _sizes(ctx_len, "ctx_len")[0]
+    shape = (rows, cache.heads, cache.head_dim)
+    pk, sk = _view(k_out, "k_out", cache.dtype, shape, dev)
+    pv, sv = _view(v_out, "v_out", cache.dtype, shape, dev)
+    s = _common(sk, sv, shape, "k_out and v_out")
+    pt, ts, tw = _table(table, B, dev)
+    a = ReadArgs(pt, ts, tw, _dense(ctx_len, "ctx_len", I32, (B,), dev), _opt(start, "start", I32, (B,), dev),
+                 _dense(cu, "cu", I32, (B + 1,), dev), pk, pv, s[0], s[1], B, rows)
+    _borrow(ctx, table, ctx_len, cu, k_out, v_out, start, *cache.tensors())
+    ctx.check(lib().pi_kv_read(ctx.handle, cache.handle, ctypes.byref(a)))
+
+
 class Attn(_Handle):
-    """A pi_attn: tree attention of ``heads`` query heads over a cache, with its scratch for up to
+    """A pi_attn: tree attention of ``heads`` query heads over a cache of either kind, with its scratch for up to
     ``max_batch`` sequences of ``max_nodes`` new nodes. ``scale`` defaults to head_dim ** -0.5."""
 
     _destroy = "pi_attn_destroy"
@@ -183,8 +239,77 @@ def tree_attention(ctx, attn: Attn, q: torch.Tensor, k_new: torch.Tensor, v_new:
     pt, ts, tw = _table(table, B, dev)
     a = AttnArgs(pq, sq[0], sq[1], sq[2], pk, pv, s[0], s[1], s[2], _opt(tree, "tree", I64, (B, N), dev), pt, ts, tw,
                  _dense(ctx_len, "ctx_len", I32, (B,), dev), po, so[0], so[1], so[2], B, N)
-    _borrow(ctx, q, k_new, v_new, tree, table, ctx_len, out, cache.k, cache.v)
+    _borrow(ctx, q, k_new, v_new, tree, table, ctx_len, out, *cache.tensors())
     ctx.check(lib().pi_tree_attention(ctx.handle, attn.handle, ctypes.byref(a)))
+
+
+class PromptAttn(_Handle):
+    """A pi_prompt: causal attention of packed prompts with ``heads`` query heads over ``kv_heads``, for up to
+    ``max_tokens`` queries of ``max_batch`` sequences. ``scale`` defaults to head_dim ** -0.5."""
+
+    _destroy = "pi_prompt_destroy"
+
+    def __init__(self, ctx, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype, max_tokens: int, max_batch: int,
+                 scale: Optional[float] = None):
+        if dtype not in (torch.float16, torch.bfloat16):
+            _bad(f"dtype is {dtype}, need fp16 or bf16")
+        self.ctx, self.heads, self.kv_heads, self.head_dim, self.dtype = ctx, heads, kv_heads, head_dim, dtype
+        scale = head_dim ** -0.5 if scale is None else scale
+        h = c_void_p()
+        ctx.check(lib().pi_prompt_create(ctx.handle, DTYPE[dtype], heads, kv_heads, head_dim, max_tokens, max_batch, scale,
+                                         ctypes.byref(h)))
+        self.handle = h
+
+
+def prompt_attention(ctx, prompt: PromptAttn, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                     cu_k: Optional[torch.Tensor], out: torch.Tensor):
+    """pi_prompt_attention: ``out`` [rows][heads][head_dim] of packed sequences, whose queries are rows ``cu_q[b]`` to
+    ``cu_q[b + 1]`` of ``q`` and whose keys are rows ``cu_k[b]`` to ``cu_k[b + 1]`` of ``k`` and ``v`` (None: the
+    same); a sequence's queries are the last ones of its keys."""
+    if q.dim() != 3 or k.dim() != 3 or cu_q.dim() != 1:
+        _bad("q and k must be [rows][heads][head_dim] and cu_q [B + 1]")
+    dev, T, Tk, B = ctx.device, _sizes(q, "q")[0], _sizes(k, "k")[0], _sizes(cu_q, "cu_q")[0] - 1
+    shape, kv = (T, prompt.heads, prompt.head_dim), (Tk, prompt.kv_heads, prompt.head_dim)
+    pq, sq = _view(q, "q", prompt.dtype, shape, dev)
+    po, so = _view(out, "out", prompt.dtype, shape, dev)
+    pk, sk = _view(k, "k", prompt.dtype, kv, dev)
+    pv, sv = _view(v, "v", prompt.dtype, kv, dev)
+    a = PromptArgs(pq, sq[0], sq[1], pk, sk[0], sk[1], pv, sv[0], sv[1], po, so[0], so[1], _dense(cu_q, "cu_q", I32, (B + 1,), dev),
+                   _opt(cu_k, "cu_k", I32, (B + 1,), dev), B, T, Tk)
+    _borrow(ctx, q, k, v, cu_q, cu_k, out)
+    ctx.check(lib().pi_prompt_attention(ctx.handle, prompt.handle, ctypes.byref(a)))
+
+
+def qk_norm_rope(ctx, q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: Optional[torch.Tensor],
+                 inv_freq: Optional[torch.Tensor], q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor],
+                 q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """pi_qk_norm_rope: heads of ``q`` and ``k`` [T][heads][head_dim] (either may be None), normalised where ``q_norm``
+    or ``k_norm`` (fp32 [head_dim]) is given, their first 2 * len(``inv_freq``) elements turned by the angles
+    ``pos[t] * inv_freq[i]``; into ``q_out`` and ``k_out``, which may be ``q`` and ``k`` themselves."""
+    x, y = (q, q_out) if q is not None else (k, k_out)
+    if x is None or y is None or x.dim() != 3 or x.dtype not in DTYPE or y.dtype not in DTYPE:
+        _bad("q and k must be floating-point tensors [T][heads][head_dim], their outputs alike")
+    dev, (T, _, D) = ctx.device, _sizes(x, "q" if q is not None else "k")
+    side = []
+    for n, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            side.append((None, (0, 0), None, (0, 0), 0))
+            continue
+        shape = (T, _sizes(t, n)[1] if t.dim() == 3 else 0, D)
+        side.append((*_view(t, n, x.dtype, shape, dev), *_view(o, n + "_out", y.dtype, shape, dev), shape[1]))
+    (pq, sq, pqo, sqo, H), (pk, sk, pko, sko, HK) = side
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        if rot > D:
+            _bad(f"inv_freq has {inv_freq.numel()} angles for heads of {D}")
+    a = RopeArgs(pq, pk, sq[0], sq[1], sk[0], sk[1], pqo, pko, sqo[0], sqo[1], sko[0], sko[1], DTYPE[x.dtype], DTYPE[y.dtype],
+                 _opt(q_norm, "q_norm", F32, (D,), dev), _opt(k_norm, "k_norm", F32, (D,), dev), eps,
+                 _dense(pos, "pos", I32, (T,), dev) if rot else None, _opt(inv_freq, "inv_freq", F32, (rot // 2,), dev), rot,
+                 int(interleaved), T, H, HK, D)
+    _borrow(ctx, q, k, pos, inv_freq, q_out, k_out, q_norm, k_norm)
+    ctx.check(lib().pi_qk_norm_rope(ctx.handle, ctypes.byref(a)))
 
 
 class Verifier(_Handle):

@@ -289,7 +289,9 @@ pi_status pi_permute_rows(pi_ctx *ctx, const void *src, void *dst, const int32_t
  * The dense operators a decoder layer needs next to the sparse FFN when it serves drafted
  * tokens: attention of a tree of tokens over a paged key/value cache, the append of the
  * accepted tokens to that cache, the check of drafted tokens against the target's
- * distribution, the residual's RMS norm with an 8-bit output, and the 8-bit matrix product.
+ * distribution, the residual's RMS norm with an 8-bit output, and the 8-bit matrix product; and for
+ * prompts and long caches the norm and rotary positions of query and key heads, causal attention of
+ * packed prompts, and the cache held in 4 bits.
  * They follow the conventions above. Tensors of these calls may be views: strides are given
  * in elements, the last axis is contiguous, and rows start at a multiple of 16 bytes unless a
  * call says otherwise. A pi_attn and a pi_verifier keep their own scratch, sized when they are
@@ -326,6 +328,33 @@ typedef struct pi_kv_desc {
 pi_status pi_kv_create(pi_ctx *ctx, const pi_kv_desc *desc, pi_kv **out);
 void pi_kv_destroy(pi_kv *kv);
 
+/* A key/value cache of one layer in 4 bits: 4.5 bits per element. Token t of page p, head h has
+ * head_dim/2 bytes of codes at p*page_stride + t*token_stride + h*head_stride and head_dim/32 fp16
+ * scales at p*scale_page_stride + t*scale_token_stride + h*scale_head_stride, k and v alike. Each block
+ * of 32 elements along the head has one scale and 16 bytes, byte j holding element j in its low half and
+ * element j + 16 in its high half; an element's value is (code - 8) * scale (the layout of PI_W_Q4_0).
+ *   dtype      PI_T_F16 or PI_T_BF16: the type of the tokens appended, read and attended with
+ *   head_dim   a multiple of 32 up to 256
+ *   strides    of the codes in bytes, multiples of 16 below 2^35; of the scales in elements below 2^35,
+ *              even where head_dim is a multiple of 64
+ * pi_kv_append writes a block so: m is its element of the largest magnitude (of two alike the positive
+ * one), scale = -m/8 rounded to bf16's 8 significant bits, at most 8160, then to fp16; code =
+ * round(x/scale) + 8 within 0..15. Every value is then an fp16 number exactly. A block with an
+ * infinity or a NaN has the scale NaN; one whose scale is 0 reads as zeros. Scales from elsewhere may be any
+ * fp16 number up to 8188 in magnitude; values are then rounded to fp16 where attention uses them.
+ * The handle is a pi_kv: pi_kv_append, pi_kv_read, pi_attn_create and pi_kv_destroy take it. A
+ * head's tokens of a page next to each other (head_stride above token_stride) read fastest. */
+typedef struct pi_kv4_desc {
+  int32_t dtype;
+  int32_t heads, head_dim, pages, page_tokens;
+  uint8_t *k, *v;
+  int64_t page_stride, token_stride, head_stride;
+  uint16_t *k_scale, *v_scale;
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} pi_kv4_desc;
+
+pi_status pi_kv4_create(pi_ctx *ctx, const pi_kv4_desc *desc, pi_kv **out);
+
 /* Append tokens to the cache: token nodes[b][j] (j itself when nodes is NULL) of sequence b's N
  * new tokens goes to position ctx_len[b] + j, for j < n[b] (all N when n is NULL).
  *   k_new, v_new  [B][N][heads][head_dim] of the cache's type, strides for both
@@ -348,11 +377,32 @@ typedef struct pi_append_args {
 
 pi_status pi_kv_append(pi_ctx *ctx, const pi_kv *kv, const pi_append_args *args);
 
+/* Read positions of a cache of either kind into packed rows: row cu[b] + i, for i below cu[b+1] -
+ * cu[b], gets the keys and values of sequence b's position start[b] + i. Rows of positions at or beyond
+ * ctx_len[b], and rows of no sequence, stay as they are; positions of pages outside the cache read as
+ * zeros. Values of a 4-bit cache are rounded to its dtype (fp16 holds them exactly).
+ *   cu         device int32 [B+1], ascending; rows outside [0, rows) are not written
+ *   start      device int32 [B] (negative: 0), or NULL: 0
+ *   ctx_len    device int32 [B], taken as 0 below 0 and as the table's positions above them
+ *   k_out, v_out  [rows][heads][head_dim] of the cache's dtype, strides for both */
+typedef struct pi_read_args {
+  const int32_t *table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t *ctx_len, *start, *cu;
+  void *k_out, *v_out;
+  int64_t out_row, out_head;
+  int32_t B, rows;
+} pi_read_args;
+
+pi_status pi_kv_read(pi_ctx *ctx, const pi_kv *kv, const pi_read_args *args);
+
 /* Attention of drafted trees over the cache. Node i of sequence b sees every cached position
  * below ctx_len[b] and the new nodes j whose bit j is set in tree[b][i]:
  *   out[b][i][h] = sum_p w_p v_p,  w = softmax over the seen p of scale * q[b][i][h] . k_p,
  * with key/value head h * kv_heads / heads. A node that sees nothing gets zeros; what is not
- * seen does not enter the result, whatever it holds.
+ * seen does not enter the result, whatever it holds. Over a 4-bit cache the cached keys and values are its
+ * values, the new nodes' are given in its dtype.
  *   heads      query heads, a multiple of the cache's heads
  *   scale      finite, above 0
  *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch */
@@ -470,6 +520,69 @@ void pi_linear_destroy(pi_linear *lin);
  *   y          [M][N] of y_dtype; rows need no alignment beyond the element's */
 pi_status pi_linear_q8(pi_ctx *ctx, pi_linear *lin, const int8_t *x, int64_t x_stride, const float *x_scale, int32_t M,
                        void *y, int32_t y_dtype, int64_t y_stride);
+
+/* Causal attention of whole prompts, packed one after another, with grouped heads. Sequence b has the
+ * queries cu_q[b]..cu_q[b+1] and the keys cu_k[b]..cu_k[b+1]; its queries are the last ones of its keys
+ * (a prompt continued after tokens held before has more keys than queries). With n queries and m keys,
+ *   out[i][h] = sum_j w_j v_j,  w = softmax over j <= i + m - n of scale * q[i][h] . k_j
+ * with key/value head h * kv_heads / heads. A query that sees no key (m < n) gets zeros; what is not
+ * seen does not enter the result, whatever it holds. Rows of no sequence stay as they are. The handle
+ * keeps its own scratch: calls that share it, and the replays of graphs that hold them, are ordered.
+ *   heads      a multiple of kv_heads;  head_dim a multiple of 8 up to 256
+ *   dtype      PI_T_F16 or PI_T_BF16;  scale finite, above 0
+ *   max_tokens, max_batch   limits of rows of q and of sequences */
+typedef struct pi_prompt pi_prompt;
+
+pi_status pi_prompt_create(pi_ctx *ctx, int32_t dtype, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                           int32_t max_tokens, int32_t max_batch, float scale, pi_prompt **out);
+void pi_prompt_destroy(pi_prompt *prompt);
+
+/*   q, out     [q_rows][heads][head_dim];  k, v [k_rows][kv_heads][head_dim]
+ *   cu_q, cu_k device int32 [B+1], ascending, cu_k NULL: cu_q; offsets are taken into [0, q_rows] and
+ *              [0, k_rows]
+ *   out may not share memory with q, k or v */
+typedef struct pi_prompt_args {
+  const void *q;
+  int64_t q_row, q_head;
+  const void *k;
+  int64_t k_row, k_head;
+  const void *v;
+  int64_t v_row, v_head;
+  void *out;
+  int64_t out_row, out_head;
+  const int32_t *cu_q, *cu_k;
+  int32_t B, q_rows, k_rows;
+} pi_prompt_args;
+
+pi_status pi_prompt_attention(pi_ctx *ctx, pi_prompt *prompt, const pi_prompt_args *args);
+
+/* RMS norm of every query and key head, and rotary positions, in one pass over T tokens:
+ *   y = x / sqrt(mean(x^2) + eps) * w      per head of head_dim elements (y = x without w)
+ *   out = y with pair i of its first `rot` elements turned by the angle pos[t] * inv_freq[i]:
+ *         (a, b) becomes (a cos - b sin, b cos + a sin)
+ * Pair i is elements i and i + rot/2, or 2i and 2i + 1 where `interleaved`. Angles are formed and
+ * reduced in 64 bits, everything else is in fp32, rounded once.
+ *   q, k       [T][heads][head_dim] and [T][kv_heads][head_dim] of x_dtype; heads or kv_heads may be 0
+ *              (q or k is not looked at); head_dim a multiple of 8 up to 512
+ *   q_out, k_out  of y_dtype; each may be its input itself, of the same type and strides
+ *   q_w, k_w   fp32 [head_dim], or NULL: no norm of these heads
+ *   pos        device int32 [T];  inv_freq device fp32 [rot/2]
+ *   rot        a multiple of 4 up to head_dim, or 0: no rotation (pos and inv_freq are not looked at) */
+typedef struct pi_rope_args {
+  const void *q, *k;
+  int64_t q_row, q_head, k_row, k_head;
+  void *q_out, *k_out;
+  int64_t q_out_row, q_out_head, k_out_row, k_out_head;
+  int32_t x_dtype, y_dtype;
+  const float *q_w, *k_w;
+  float eps;
+  const int32_t *pos;
+  const float *inv_freq;
+  int32_t rot, interleaved;
+  int32_t T, heads, kv_heads, head_dim;
+} pi_rope_args;
+
+pi_status pi_qk_norm_rope(pi_ctx *ctx, const pi_rope_args *args);
 
 #ifdef __cplusplus
 }
