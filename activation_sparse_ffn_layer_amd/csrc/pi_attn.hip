@@ -519,8 +519,9 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
   // scratch of the largest call: rows (all heads, all slots) of any number of nodes and sequences
   size_t rows = 0;
   for (int n = 1; n <= max_nodes; ++n) {
+    // over a 4-bit cache a sequence's part may end and another begin in each slot
     const AttnPlan p = (kv->q4 ? attn4_plan : attn_plan)(ctx->cus, HK, n * G, max_batch, DP);
-    rows = std::max(rows, (size_t)p.slots * HK * n * G);
+    rows = std::max(rows, (size_t)(p.slots + (kv->q4 ? max_batch : 0)) * HK * n * G);
   }
   PI_HIP(ctx, hipSetDevice(ctx->device));
   uint8_t* ws = nullptr;
@@ -575,8 +576,8 @@ pi_status pi_tree_attention(pi_ctx* ctx, pi_attn* attn, const pi_attn_args* args
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const int HK = kv->desc.heads, G = attn->heads / HK;
   const int D = kv->desc.head_dim;
-  const AttnPlan p = kv->q4 ? attn4_plan(ctx->cus, HK, a.N * G, a.B, padded_dim4(D)) : attn_plan(ctx->cus, HK, a.N * G, a.B, padded_dim(D));
   KvDev c = kv_dev(kv, a.table, a.table_stride, a.table_width);
+  const AttnPlan p = kv->q4 ? attn4_plan(ctx->cus, HK, a.N * G, a.B, padded_dim4(D)) : attn_plan(ctx->cus, HK, a.N * G, a.B, padded_dim(D));
   if (a.table == nullptr) {
     c.table = attn->self;
     c.table_stride = 1;

@@ -66,10 +66,8 @@ __device__ __forceinline__ float swap_add(float v) {
 // Tiles of KT keys that a sequence's positions and nodes take. Positions go up to 2^31 - 65 and a tile
 // or its successors may end beyond 2^31: sums of them are unsigned, and the kernels go by a tile's
 // place relative to the sequence's end, which is small where it matters.
-// Over a 4-bit cache (Q4) the new nodes, 64 at most, are a tile of their own.
-template <int KT, bool Q4 = false>
+template <int KT>
 __device__ __forceinline__ int key_tiles(const AttnDev& a, int b) {
-  if (Q4) return (int)(((uint32_t)kv_len(a.c, a.ctx_len, b) + (uint32_t)(KT - 1)) / (uint32_t)KT) + 1;
   return (int)(((uint32_t)kv_len(a.c, a.ctx_len, b) + (uint32_t)(a.N + KT - 1)) / (uint32_t)KT);
 }
 template <int KT>
@@ -91,10 +89,10 @@ __device__ __forceinline__ uint32_t sum_tiles(uint32_t n) {
 struct Chunk {
   int b, t0, t1, count, first;
 };
-template <int KT, bool Q4 = false>
+template <int KT>
 __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o) {
   const int lane = threadIdx.x % WAVE;
-  auto tiles = [&](int b) { return b < a.B ? key_tiles<KT, Q4>(a, b) : 0; };
+  auto tiles = [&](int b) { return b < a.B ? key_tiles<KT>(a, b) : 0; };
   if (a.B == 1) {
     const int t = tiles(0), c = (t + a.slots - 1) / a.slots;
     *o = Chunk{0, slot * c, min(t, slot * c + c), (t + c - 1) / c, 0};
@@ -136,35 +134,18 @@ __device__ __forceinline__ bool find_chunk(const AttnDev& a, int slot, Chunk* o)
   return false;
 }
 
-__device__ u32x4 attn_zero;  // zeros, never written
+__device__ u32x4 attn_zero[8];  // zeros, never written
 
 // LDS of a workgroup: keys, then values, of one tile (two where tiles are shared by waves). A
 // row's pitch spreads what is read at once over the 64 banks: 16 rows of 16 bytes of K, and of V,
 // by its transposing reads, 4 rows of 64 bytes.
 template <int DP> constexpr int k_pitch() { return DP * 2 + 16; }
 template <int DP> constexpr int v_pitch() { return DP * 2 % 128 == 0 ? DP * 2 + 64 : DP * 2; }
-// Bound by memory, the partial results' bytes (27 MB at 6656 rows in some 13 chunks: 10 us).
-// out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over a sequence's chunks s, one wave per
-// query row, 4 columns per lane; rows of sequences of one chunk are done already.
-template <typename T, int DP, int KT, bool Q4 = false>
-__global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
+// out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over the `count` partial results of row r from slot `first` on, by
+// one wave, 4 columns per lane.
+template <typename T, int DP>
+__device__ __forceinline__ void join_parts(const AttnDev& a, int b, int hk, int r, int first, int count) {
   const int lane = threadIdx.x % WAVE;
-  // (b, hk, r) of this wave
-  const int id = blockIdx.x * NWAVES + threadIdx.x / WAVE;
-  if (id >= rows) return;
-  const int r = id % a.R, hk = id / a.R % a.HK, b = id / a.R / a.HK;
-  // the first slot of sequence b: the chunks before it
-  auto tiles = [&](int i) { return i < a.B ? key_tiles<KT, Q4>(a, i) : 0; };
-  auto sum = [&](int c, int end) {
-    uint32_t n = 0;
-    for (int i = lane; i < end; i += WAVE) n = lane_tiles(n, (tiles(i) + c - 1) / c);
-    return sum_tiles(n);
-  };
-  const uint32_t slots = (uint32_t)a.slots;
-  int c = max(1, (int)((sum(1, a.B) + slots - 1) / slots));
-  while (c > 1 && sum(c, a.B) > slots) c += max(1, c >> 5);
-  const int first = (int)sum(c, b), count = (tiles(b) + c - 1) / c;
-  if (count == 1) return;
   const long long at0 = ((long long)first * a.HK + hk) * a.R + r, next = (long long)a.HK * a.R;
   float m = -__builtin_inff();
   for (int s = lane; s < count; s += WAVE) m = fmaxf(m, a.ml[2 * (at0 + s * next)]);
@@ -219,9 +200,34 @@ __global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
 
 constexpr int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 
+// Bound by memory, the partial results' bytes (27 MB at 6656 rows in some 13 chunks: 10 us).
+// Over a sequence's chunks, one wave per query row; rows of sequences of one chunk are done already.
+template <typename T, int DP, int KT>
+__global__ __launch_bounds__(BLOCK) void k_attn_join(AttnDev a, int rows) {
+  const int lane = threadIdx.x % WAVE;
+  // (b, hk, r) of this wave
+  const int id = blockIdx.x * NWAVES + threadIdx.x / WAVE;
+  if (id >= rows) return;
+  const int r = id % a.R, hk = id / a.R % a.HK, b = id / a.R / a.HK;
+  // the first slot of sequence b: the chunks before it
+  auto tiles = [&](int i) { return i < a.B ? key_tiles<KT>(a, i) : 0; };
+  auto sum = [&](int c, int end) {
+    uint32_t n = 0;
+    for (int i = lane; i < end; i += WAVE) n = lane_tiles(n, (tiles(i) + c - 1) / c);
+    return sum_tiles(n);
+  };
+  const uint32_t slots = (uint32_t)a.slots;
+  int c = max(1, (int)((sum(1, a.B) + slots - 1) / slots));
+  while (c > 1 && sum(c, a.B) > slots) c += max(1, c >> 5);
+  const int first = (int)sum(c, b), count = (tiles(b) + c - 1) / c;
+  if (count == 1) return;
+  join_parts<T, DP>(a, b, hk, r, first, count);
+}
+
 }  // namespace
 
-// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences).
+// How a call is cut: waves along the rows, row tiles and slots (chunks of all sequences;
+// over a 4-bit cache spans of all sequences' tiles).
 struct AttnPlan {
   int wq, row_tiles, slots;
 };

@@ -235,10 +235,10 @@ pi_status pi_kv4_create(pi_ctx* ctx, const pi_kv4_desc* desc, pi_kv** out) {
   if (d.scale_page_stride < 0 || d.scale_token_stride < 0 || d.scale_head_stride < 0 ||
       (d.head_dim % 64 == 0 && ((d.scale_page_stride | d.scale_token_stride | d.scale_head_stride) & 1)))
     return fail(ctx, PI_ERR_INVALID, "strides of the scales must be even");
-  const int64_t far = 1ll << 35;
-  if (d.page_stride >= far || d.token_stride >= far || d.head_stride >= far || d.scale_page_stride >= far ||
-      d.scale_token_stride >= far || d.scale_head_stride >= far)
-    return fail(ctx, PI_ERR_UNSUPPORTED, "strides are below 2^35");
+  if (d.page_stride >= 1ll << 35 || d.token_stride >= 1ll << 35 || d.head_stride >= 1ll << 35)
+    return fail(ctx, PI_ERR_UNSUPPORTED, "strides of the codes are below 2^35");
+  if (d.scale_page_stride >= 1ll << 32 || d.scale_token_stride >= 1ll << 32 || d.scale_head_stride >= 1ll << 32)
+    return fail(ctx, PI_ERR_UNSUPPORTED, "strides of the scales are below 2^32");
   PI_TRY(check_dev_ptr(ctx, d.k, "k"));
   PI_TRY(check_dev_ptr(ctx, d.v, "v"));
   PI_TRY(check_dev_ptr(ctx, d.k_scale, "k_scale"));

@@ -81,19 +81,6 @@ struct Kv4Dev {
 };
 inline Kv4Dev kv4_dev(const pi_kv* kv) { return Kv4Dev{kv->k_scale, kv->v_scale, kv->scale_page, kv->scale_token, kv->scale_head}; }
 
-// Four code bytes of a block (byte j: element j | element j + 16 << 4) as 8 fp16 values (code - 8) in
-// pairs: out[0] elements j, j+2; out[1] j+1, j+3; out[2] 16+j, 16+j+2; out[3] 16+j+1, 16+j+3. A
-// nibble in the low mantissa bits of 1024 stands for 1024 + code, four bits further up for 1024 + 16 code.
-__device__ __forceinline__ void q4_pairs(uint32_t w, half2_t (&out)[4]) {
-  const uint32_t u = w >> 8;
-  const half2_t lo = (half2_t){(half_t)1032.f, (half_t)1032.f}, sixteenth = (half2_t){(half_t)0.0625f, (half_t)0.0625f},
-                hi = (half2_t){(half_t)-72.f, (half_t)-72.f};
-  out[0] = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u) - lo;
-  out[1] = __builtin_bit_cast(half2_t, (u & 0x000F000Fu) | 0x64006400u) - lo;
-  out[2] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u), sixteenth, hi);
-  out[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (u & 0x00F000F0u) | 0x64006400u), sixteenth, hi);
-}
-
 // Strides of a [B][N][heads][D] tensor of 16-bit elements whose rows are 16-byte aligned.
 inline pi_status check_bnh(pi_ctx* c, const char* name, const void* p, int64_t sb, int64_t sn, int64_t sh) {
   PI_TRY(check_dev_ptr(c, p, name));

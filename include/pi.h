@@ -335,7 +335,7 @@ void pi_kv_destroy(pi_kv *kv);
  * element j + 16 in its high half; an element's value is (code - 8) * scale (the layout of PI_W_Q4_0).
  *   dtype      PI_T_F16 or PI_T_BF16: the type of the tokens appended, read and attended with
  *   head_dim   a multiple of 32 up to 256
- *   strides    of the codes in bytes, multiples of 16 below 2^35; of the scales in elements below 2^35,
+ *   strides    of the codes in bytes, multiples of 16 below 2^35; of the scales in elements below 2^32,
  *              even where head_dim is a multiple of 64
  * pi_kv_append writes a block so: m is its element of the largest magnitude (of two alike the positive
  * one), scale = -m/8 rounded to bf16's 8 significant bits, at most 8160, then to fp16; code =
