@@ -2,13 +2,15 @@
 //
 // y = x / sqrt(mean(x^2) + eps) * w per head, then each pair (a, b) of the first rot elements turns by
 // pos * inv_freq: (a cos - b sin, b cos + a sin). Bound by memory: a head is read once, kept in
-// registers and written once. A lane has the same 2U elements of every head it takes (U pairs: two
-// pieces of U elements each, U * i and rot/2 + U * i, or 2U in a row where pairs are interleaved), so
-// a token's sines and cosines are worked out once per wave and serve all its heads.
+// registers and written once. A workgroup takes up to ROPE_TOKENS tokens; it works their sines and cosines out first, one
+// angle a thread, into LDS. A lane then has the same 2U elements of every head it takes (U pairs: two pieces of U elements
+// each, U * i and rot/2 + U * i, or 2U in a row where pairs are interleaved), HEADS_AHEAD heads in flight.
 //
 // The angle is a whole number times an fp32 number, exact in 64 bits up to 2^29 and off by 2^-53 of
 // itself beyond; as turns, reduced by its nearest whole number, it goes on in fp32 (2^-25 of a turn).
-#include "pi_host.hpp"
+#include <algorithm>
+
+#include "pi_kv.hpp"
 #include "pi_types.hpp"
 
 using namespace pi;
@@ -27,7 +29,8 @@ struct RopeDev {
   const int32_t* pos;
   const float* inv_freq;
   float eps;
-  int heads, kv_heads, D, rot, per_wave;  // per_wave: heads that one wave takes, one group of lanes after another
+  PageDiv by_heads;                              // heads of a token
+  int T, heads, kv_heads, D, rot, tokens, part;  // tokens of a workgroup, and of their heads (all tokens') it takes
 };
 
 template <typename T, int U> struct Piece { typedef T type __attribute__((ext_vector_type(U))); };
@@ -54,14 +57,62 @@ __device__ __forceinline__ void store_piece(T* p, const float (&o)[U]) {
   }
 }
 
-// LPH lanes per head, a power of two. Heads are numbered queries first, then keys.
+// A head's norm and weights; its elements are in LPH lanes.
+template <int U, int LPH>
+__device__ __forceinline__ void normalise(const RopeDev& p, const RopeSide& side, int a0, int b0, float (&a)[U], float (&b)[U]) {
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < U; ++i) ss += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+  for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor(ss, o, WAVE);
+  const float mean = ss / (float)p.D + p.eps;
+  float rinv = mean == 0.f ? 0.f : 1.0f / sqrtf(mean);  // a head of zeros, without eps: zeros
+  const bool far = !(ss < __builtin_inff()) || mean < 1e-30f;
+  if (__any(far)) {
+    // squares beyond fp32's range, or lost below it: again with the head times a power of two that brings its largest
+    // element, or eps's root where that is larger, near 1
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) big = fmaxf(big, fmaxf(fabsf(a[i]), fabsf(b[i])));
+#pragma unroll
+    for (int o = 1; o < LPH; o <<= 1) big = fmaxf(big, __shfl_xor(big, o, WAVE));
+    const bool again = far && ss == ss && big > 0.f && big < __builtin_inff();
+    const int e = again ? -ilogbf(fmaxf(big, sqrtf(p.eps))) : 0;
+    float s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float x = ldexpf(a[i], e), y = ldexpf(b[i], e);
+      s2 += x * x + y * y;
+      if (side.w != nullptr) {
+        a[i] = x;
+        b[i] = y;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < LPH; o <<= 1) s2 += __shfl_xor(s2, o, WAVE);
+    if (again) rinv = 1.0f / sqrtf(s2 / (float)p.D + ldexpf(ldexpf(p.eps, e), e));
+  }
+  if (side.w == nullptr) return;
+  float wa[U], wb[U];
+  load_piece<U>(side.w + a0, wa);
+  load_piece<U>(side.w + b0, wb);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    a[i] = a[i] * rinv * wa[i];
+    b[i] = b[i] * rinv * wb[i];
+  }
+}
+
+constexpr int ROPE_TOKENS = 8, HEADS_AHEAD = 2;
+
+// LPH lanes per head, a power of two. Heads are numbered token by token, queries first, then keys.
 template <typename TX, typename TY, int U, bool PAIRS, int LPH>
 __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
-  constexpr int HPW = WAVE / LPH;  // heads of a wave at once
-  const long long t = blockIdx.x;
-  const int lane = threadIdx.x % WAVE, slot = lane % LPH;
-  const int half = p.rot >> 1, turning = half / U;
-  const bool turns = slot < turning, live = slot < p.D / (2 * U);
+  extern __shared__ float turn[];  // [tokens][2][half]: cosines, sines
+  constexpr int HPB = BLOCK / LPH;
+  const int t0 = blockIdx.x * p.tokens, tokens = min(p.tokens, p.T - t0);
+  const int half = p.rot >> 1, slot = threadIdx.x % LPH;
+  const bool turns = slot < half / U, live = slot < p.D / (2 * U);
   int a0, b0;  // first elements of this lane's two pieces
   if (PAIRS || !turns) {
     a0 = 2 * U * slot;
@@ -71,122 +122,92 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
     b0 = half + a0;
   }
   if (!live) a0 = b0 = 0;
-  const int first = (blockIdx.y * NWAVES + threadIdx.x / WAVE) * p.per_wave + lane / LPH;
   const int total = p.heads + p.kv_heads;
-  if (first - lane / LPH >= total) return;
-
-  float c[U], s[U];
+  const int first = blockIdx.y * p.part + threadIdx.x / LPH, end = min((int)(blockIdx.y + 1) * p.part, tokens * total);
+  float a[HEADS_AHEAD][U], b[HEADS_AHEAD][U];
+  int tok[HEADS_AHEAD], head[HEADS_AHEAD];
+  bool in[HEADS_AHEAD], key[HEADS_AHEAD];
+  auto load = [&](int h0) {
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
-  if (turns) {
-    float f[U];
-    const double at = (double)p.pos[t];
-    load_piece<U>(p.inv_freq + U * slot, f);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const double turn = at * (double)f[i] * 0.15915494309189533577;  // 1 / (2 pi)
-      sincospif(2.f * (float)(turn - rint(turn)), &s[i], &c[i]);
-    }
-  }
-  for (int j = 0; j < p.per_wave; j += HPW) {
-    const int h = first + j;
-    if (first - lane / LPH + j >= total) return;  // the wave's last heads
-    const bool in = live && h < total;
-    const bool key = h >= p.heads;
-    const RopeSide& side = key ? p.k : p.q;
-    const int hh = in ? (key ? h - p.heads : h) : 0;
-    float a[U], b[U];
-    if (in) {
-      const TX* x = static_cast<const TX*>(side.x) + t * side.row + hh * side.head;
-      load_piece<U>(x + a0, a);
-      load_piece<U>(x + b0, b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < U; ++i) a[i] = b[i] = 0.f;
-    }
-    if (p.q.w != nullptr || p.k.w != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < U; ++i) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor(ss, o, WAVE);
-      const float mean = ss / (float)p.D + p.eps;
-      float rinv = mean == 0.f ? 0.f : 1.0f / sqrtf(mean);  // a head of zeros, without eps: zeros
-      if (__any(!(ss < __builtin_inff()) || mean < 1e-30f)) {
-        // squares beyond fp32's range, or lost below it: again with the head times a power of two that brings
-        // its largest element, or eps's root where that is larger, near 1
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < U; ++i) big = fmaxf(big, fmaxf(fabsf(a[i]), fabsf(b[i])));
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) big = fmaxf(big, __shfl_xor(big, o, WAVE));
-        const bool again = (!(ss < __builtin_inff()) || mean < 1e-30f) && ss == ss && big > 0.f && big < __builtin_inff();
-        const int e = again ? -ilogbf(fmaxf(big, sqrtf(p.eps))) : 0;
-        float s2 = 0.f;
-        const bool wanted = (key ? p.k.w : p.q.w) != nullptr;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const float x = ldexpf(a[i], e), y = ldexpf(b[i], e);
-          s2 += x * x + y * y;
-          if (wanted && again) {
-            a[i] = x;
-            b[i] = y;
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) s2 += __shfl_xor(s2, o, WAVE);
-        if (again) rinv = 1.0f / sqrtf(s2 / (float)p.D + ldexpf(ldexpf(p.eps, e), e));
-      }
-      if (side.w != nullptr) {
-        float wa[U], wb[U];
-        load_piece<U>(side.w + a0, wa);
-        load_piece<U>(side.w + b0, wb);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          a[i] = a[i] * rinv * wa[i];
-          b[i] = b[i] * rinv * wb[i];
-        }
-      }
-    }
-    if (!in) continue;
-    TY* y = static_cast<TY*>(side.y) + t * side.out_row + hh * side.out_head;
-    if (turns) {
-      if constexpr (PAIRS) {  // a and b are 2U elements in a row: pairs (0, 1), (2, 3), ..
-#pragma unroll
-        for (int i = 0; i < U / 2; ++i) {
-          const float a0v = a[2 * i], b0v = b[2 * i];
-          a[2 * i] = a0v * c[i] - a[2 * i + 1] * s[i];
-          a[2 * i + 1] = a[2 * i + 1] * c[i] + a0v * s[i];
-          b[2 * i] = b0v * c[U / 2 + i] - b[2 * i + 1] * s[U / 2 + i];
-          b[2 * i + 1] = b[2 * i + 1] * c[U / 2 + i] + b0v * s[U / 2 + i];
-        }
+    for (int n = 0; n < HEADS_AHEAD; ++n) {
+      const int h = h0 + n * HPB;
+      in[n] = live && h < end;
+      uint32_t hh;
+      tok[n] = (int)page_of(p.by_heads, in[n] ? (uint32_t)h : 0u, &hh);
+      key[n] = (int)hh >= p.heads;
+      head[n] = (int)hh - (key[n] ? p.heads : 0);
+      const RopeSide& side = key[n] ? p.k : p.q;
+      if (in[n]) {
+        const TX* x = static_cast<const TX*>(side.x) + (long long)(t0 + tok[n]) * side.row + head[n] * side.head;
+        load_piece<U>(x + a0, a[n]);
+        load_piece<U>(x + b0, b[n]);
       } else {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const float av = a[i];
-          a[i] = av * c[i] - b[i] * s[i];
-          b[i] = b[i] * c[i] + av * s[i];
-        }
+        for (int i = 0; i < U; ++i) a[n][i] = b[n][i] = 0.f;
       }
     }
-    store_piece<U>(y + a0, a);
-    store_piece<U>(y + b0, b);
+  };
+  load(first);  // before the angles, whose arithmetic takes as long
+  for (int i = threadIdx.x; i < tokens * half; i += BLOCK) {
+    const int t = i / half, k = i - t * half;
+    const double turns = (double)p.pos[t0 + t] * (double)p.inv_freq[k] * 0.15915494309189533577;  // 1 / (2 pi)
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    turn[2 * t * half + k] = c;
+    turn[(2 * t + 1) * half + k] = s;
+  }
+  __syncthreads();
+  for (int h0 = first; h0 - (int)threadIdx.x / LPH < end; h0 += HEADS_AHEAD * HPB) {
+    if (h0 != first) load(h0);
+#pragma unroll
+    for (int n = 0; n < HEADS_AHEAD; ++n) {
+      const RopeSide& side = key[n] ? p.k : p.q;
+      if (p.q.w != nullptr || p.k.w != nullptr) normalise<U, LPH>(p, side, a0, b0, a[n], b[n]);
+      if (!in[n]) continue;
+      if (turns) {
+        float c[U], s[U];
+        const float* at = turn + 2 * tok[n] * half + U * slot;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          c[i] = at[i];
+          s[i] = at[half + i];
+        }
+        if constexpr (PAIRS) {  // a and b are 2U elements in a row: pairs (0, 1), (2, 3), ..
+#pragma unroll
+          for (int i = 0; i < U / 2; ++i) {
+            const float av = a[n][2 * i], bv = b[n][2 * i];
+            a[n][2 * i] = av * c[i] - a[n][2 * i + 1] * s[i];
+            a[n][2 * i + 1] = a[n][2 * i + 1] * c[i] + av * s[i];
+            b[n][2 * i] = bv * c[U / 2 + i] - b[n][2 * i + 1] * s[U / 2 + i];
+            b[n][2 * i + 1] = b[n][2 * i + 1] * c[U / 2 + i] + bv * s[U / 2 + i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const float av = a[n][i];
+            a[n][i] = av * c[i] - b[n][i] * s[i];
+            b[n][i] = b[n][i] * c[i] + av * s[i];
+          }
+        }
+      }
+      TY* y = static_cast<TY*>(side.y) + (long long)(t0 + tok[n]) * side.out_row + head[n] * side.out_head;
+      store_piece<U>(y + a0, a[n]);
+      store_piece<U>(y + b0, b[n]);
+    }
   }
 }
 
 template <typename TX, typename TY, int U, bool PAIRS, int LPH>
 pi_status launch_rope(pi_ctx* c, RopeDev p, int T) {
-  constexpr int HPW = WAVE / LPH;
-  const int total = p.heads + p.kv_heads, groups = (total + HPW - 1) / HPW;
-  // A wave takes as many heads as leave 8 waves for each SIMD: the sines are worked out once per wave.
-  int rounds = 1;
-  while (rounds < groups && (long long)T * ((groups + 2 * rounds - 1) / (2 * rounds)) >= 32ll * c->cus) rounds *= 2;
-  p.per_wave = rounds * HPW;
-  const int waves = (groups + rounds - 1) / rounds;
-  PI_HIP(c, launch_k(c, 0, k_qk_norm_rope<TX, TY, U, PAIRS, LPH>, dim3(T, (waves + NWAVES - 1) / NWAVES), 0, p));
+  constexpr int HPB = BLOCK / LPH;
+  const int total = p.heads + p.kv_heads;
+  // As many tokens as leave 4 workgroups for each CU, and no more than heads in flight need; then, where there are few
+  // tokens, their heads in parts of as many as a workgroup has lanes for.
+  p.tokens = std::max(1, std::min({ROPE_TOKENS, T / (4 * c->cus), (HEADS_AHEAD * HPB * 2 + total - 1) / total}));
+  p.part = p.tokens > 1 ? p.tokens * total : HEADS_AHEAD * HPB;
+  p.by_heads = page_div(total);
+  const dim3 grid((T - 1) / p.tokens + 1, (p.tokens * total - 1) / p.part + 1);
+  PI_HIP(c, launch_k(c, 0, k_qk_norm_rope<TX, TY, U, PAIRS, LPH>, grid, p.tokens * p.rot * sizeof(float), p));
   return PI_OK;
 }
 
@@ -263,7 +284,7 @@ extern "C" pi_status pi_qk_norm_rope(pi_ctx* ctx, const pi_rope_args* args) {
   PI_HIP(ctx, hipSetDevice(ctx->device));
   const RopeDev p{{a.q, a.q_out, a.heads > 0 ? a.q_w : nullptr, a.q_row, a.q_head, a.q_out_row, a.q_out_head},
                   {a.k, a.k_out, a.kv_heads > 0 ? a.k_w : nullptr, a.k_row, a.k_head, a.k_out_row, a.k_out_head},
-                  a.pos, a.inv_freq, a.eps, a.heads, a.kv_heads, a.head_dim, a.rot, 0};
+                  a.pos, a.inv_freq, a.eps, PageDiv{}, a.T, a.heads, a.kv_heads, a.head_dim, a.rot, 0, 0};
   switch (a.x_dtype) {
     case PI_T_F32: return launch_rope_x<float>(ctx, p, a.T, a.y_dtype, a.interleaved != 0);
     case PI_T_F16: return launch_rope_x<half_t>(ctx, p, a.T, a.y_dtype, a.interleaved != 0);
