@@ -17,16 +17,43 @@ struct pi_prompt {
   pi_ctx* ctx;
   int dtype, heads, kv_heads, head_dim, max_tokens, max_batch;
   float scale;
+  uint8_t* ws;      // partial results of split keys
+  size_t ws_rows;   // query rows times splits that it holds
 };
 
 namespace {
+
+constexpr int SPLITS = 32;  // at most
+
+// How a call is cut. Eight waves a workgroup where their row tiles fill the chip, else four: more workgroups, and tiles that
+// fit short sequences (500 tokens of 32 heads: 21 us, with eight 26; with two, whose threads have too many rows to load,
+// 30). Where those are still few, the keys are split, four tiles at least a part: 33 tokens after 8192 held ones, 64 heads
+// (8 kv), take 40 us, with whole rows 238.
+struct PromptPlan {
+  int wq, tiles, splits;
+};
+PromptPlan prompt_plan(int cus, int HK, int G, int DP, int rows, int B, int64_t keys) {
+  PromptPlan p;
+  const int64_t r = (int64_t)rows * G;
+  for (p.wq = 8;; p.wq = 4) {
+    // every sequence's last tile may be a part of one
+    p.tiles = (int)((r + 32 * p.wq - 1) / (32 * p.wq)) + B - 1;
+    if (DP > 128 || p.wq == 4 || (r / (32 * p.wq) * HK >= cus && r > 128ll * B)) break;
+  }
+  const int64_t full = std::max<int64_t>(1, (r + 32 * p.wq - 1) / (32 * p.wq)) * HK;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({SPLITS, (p.wq == 8 ? 1 : 2) * cus / full, keys / B / (4 * 64)}));
+  return p;
+}
+
 
 struct PromptDev {
   const uint8_t *q, *k, *v;
   uint8_t* out;
   const int32_t *cu_q, *cu_k;
   long long q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+  float *part, *ml;                        // of split keys: partial results [row][head][split][DP], maximum and sum
   int B, q_rows, k_rows, HK, G, D, tiles;  // tiles: row tiles, an upper limit
+  int splits;                              // parts that a row tile's keys are cut into, a workgroup each
   float scale2;  // scale * log2(e)
 };
 
@@ -52,9 +79,9 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int s_odd;  // a value row that not every row sees holds an infinity or a NaN
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, half = lane >> 5, l32 = lane & 31;
-  const int hk = blockIdx.x % a.HK;
+  const int hk = blockIdx.x % a.HK, split = blockIdx.x / a.HK % a.splits;
   // the row tiles from the last one on: those with the most keys start first
-  const int slot = a.tiles - 1 - blockIdx.x / a.HK;
+  const int slot = a.tiles - 1 - blockIdx.x / a.HK / a.splits;
   int b = -1, rt = 0, before = 0;
   for (int b0 = 0; b0 < a.B; b0 += WAVE) {
     int first;
@@ -88,7 +115,10 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int nk = min(max(min(Lq, (row0 + R - 1) / a.G + 1) + ahead, 0), Lk);  // keys that some row sees
   const int all = row0 / a.G + ahead;                                         // the last one that all see
   const int wall = wrow0 / a.G + ahead, wmost = min(Lq - 1, (wrow0 + 31) / a.G) + ahead;
+  // this workgroup's part of the key tiles
   const int ntiles = (nk + KT - 1) / KT;
+  const int t0 = a.splits == 1 ? 0 : (int)((long long)ntiles * split / a.splits);
+  const int t1 = a.splits == 1 ? ntiles : (int)((long long)ntiles * (split + 1) / a.splits);
 
   v8 qf[KS];
   {
@@ -101,24 +131,42 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
   }
 
   typedef const __attribute__((address_space(1))) uint8_t* gp;  // global by type: a generic load counts as LDS too
-  const gp zero = (gp)(const uint8_t*)&attn_zero;
   const int lr = (int)threadIdx.x / LPR, lc = (int)threadIdx.x % LPR;
   const bool piece_in = 8 * lc < a.D;
-  const gp kg = (gp)a.k + 2 * ((long long)k0 * a.k_row + (long long)hk * a.k_head + (piece_in ? 8 * lc : 0));
-  const gp vg = (gp)a.v + 2 * ((long long)k0 * a.v_row + (long long)hk * a.v_head + (piece_in ? 8 * lc : 0));
-  u32x4 kr[2][PASS], vr[2][PASS];
-  auto load = [&](int tile, int set) {
+  // Rows of a tile are at a scalar address plus the lane's offset, which is the same for all tiles but the last: rows
+  // past the keys that some row sees stand for the last such key there. They weigh nothing.
+  const gp kg = (gp)a.k + 2 * ((long long)k0 * a.k_row + (long long)hk * a.k_head);
+  const gp vg = (gp)a.v + 2 * ((long long)k0 * a.v_row + (long long)hk * a.v_head);
+  const uint32_t kstep = 2 * (uint32_t)a.k_row, vstep = 2 * (uint32_t)a.v_row, lp = piece_in ? 16 * lc : 0;
+  uint32_t ko[PASS], vo[PASS];
 #pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int j = tile * KT + lr + i * RPP;
-      const bool in = piece_in && j < nk;
-      const gp k = in ? kg + 2 * j * a.k_row : zero, v = in ? vg + 2 * j * a.v_row : zero;
-      kr[set][i] = *(const __attribute__((address_space(1))) u32x4*)k;
-      vr[set][i] = *(const __attribute__((address_space(1))) u32x4*)v;
+  for (int i = 0; i < PASS; ++i) {
+    ko[i] = (uint32_t)(lr + i * RPP) * kstep + lp;
+    vo[i] = (uint32_t)(lr + i * RPP) * vstep + lp;
+  }
+  // rows on their way to LDS: of the next two tiles, of one where a thread has many
+  constexpr int SETS = WQ == 8 && DP <= 128 ? 2 : 1;
+  u32x4 kr[SETS][PASS], vr[SETS][PASS];
+  auto load_rows = [&](gp base, long long row, uint32_t step, const uint32_t (&at)[PASS], int tile, u32x4 (&r)[PASS]) __attribute__((always_inline)) {
+    if (tile >= t1) return;
+    const gp p = base + 2 * (long long)(tile * KT) * row;
+    if (tile * KT + KT <= nk) {
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) r[i] = *(const __attribute__((address_space(1))) u32x4*)(p + at[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PASS; ++i)
+        r[i] = *(const __attribute__((address_space(1))) u32x4*)(p + (uint32_t)min(lr + i * RPP, nk - 1 - tile * KT) * step + lp);
     }
   };
-  auto store = [&](int tile, int stage, int set) {
-    uint8_t* base = smem + stage * STAGE;
+  auto load_k = [&](int tile, int set) __attribute__((always_inline)) { load_rows(kg, a.k_row, kstep, ko, tile, kr[set]); };
+  auto load_v = [&](int tile, int set) __attribute__((always_inline)) { load_rows(vg, a.v_row, vstep, vo, tile, vr[set]); };
+  auto store_k = [&](uint8_t* to, int set) {
+#pragma unroll
+    for (int i = 0; i < PASS; ++i)
+      if (piece_in) *reinterpret_cast<u32x4*>(to + (lr + i * RPP) * KP + lc * 16) = kr[set][i];
+  };
+  auto store_v = [&](int tile, uint8_t* to, int set) {
     if (tile * KT + KT - 1 > all) {
       // A weight of zero times an infinity or a NaN is a NaN: such elements of keys that not every row sees
       // stay out of the product and are added to the rows that see them at the end.
@@ -134,13 +182,8 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
     }
 #pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int r = lr + i * RPP;
-      if (DP / 8 == LPR || lc < DP / 8) {
-        *reinterpret_cast<u32x4*>(base + r * KP + lc * 16) = kr[set][i];
-        *reinterpret_cast<u32x4*>(base + KT * KP + r * VP + lc * 16) = vr[set][i];
-      }
-    }
+    for (int i = 0; i < PASS; ++i)
+      if (piece_in) *reinterpret_cast<u32x4*>(to + (lr + i * RPP) * VP + lc * 16) = vr[set][i];
   };
 
   f32x16 o[DB];
@@ -148,10 +191,9 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
   for (int i = 0; i < DB; ++i) o[i] = (f32x16){};
   float m = -__builtin_inff(), l = 0.f;  // running maximum (log2 domain); this half's sum
 
-  auto compute = [&](int tile, int stage) {
-    const uint8_t* kb0 = smem + stage * STAGE;
-    const uint8_t* vb0 = kb0 + KT * KP;
-    f32x16 s[KB];
+  f32x16 s[KB];
+  v8 pf[KB][2];
+  auto scores = [&](const uint8_t* kb0) __attribute__((always_inline)) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       s[kb] = (f32x16){};
@@ -159,6 +201,8 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
       for (int i = 0; i < KS; ++i)
         s[kb] = Mm<T>::mfma(__builtin_bit_cast(v8, ld16(kb0 + (kb * 32 + l32) * KP + 32 * i + 16 * half)), qf[i], s[kb]);
     }
+  };
+  auto weights = [&](int tile) __attribute__((always_inline)) {
     if (tile * KT + KT - 1 > wall) {
       const int last = lim - tile * KT;
       const uint64_t seen = last >= 63 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1;
@@ -187,7 +231,6 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
     }
     m = mn;
-    v8 pf[KB][2];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -196,6 +239,8 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         l += w;
         pf[kb][r >> 3][r & 7] = (T)w;
       }
+  };
+  auto values = [&](const uint8_t* vb0) __attribute__((always_inline)) {
     const uint8_t* vl = vb0 + (4 * half + ((lane & 15) >> 2)) * VP + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -212,32 +257,51 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
   };
 
-  if (ntiles > 0) {
-    load(0, 0);
-    load(1, 1);
-    __syncthreads();  // s_odd is 0
-    store(0, 0, 0);
+  // what lies past the heads' last element in LDS is never stored to: zeros
+  if (a.D < DP && t0 < t1)
+    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += NT) *reinterpret_cast<u32x4*>(smem + 16 * i) = (u32x4){0, 0, 0, 0};
+  if (t0 >= t1) {
     __syncthreads();
-    auto step = [&](int t, int h) {
-      load(t + 2, h);
+  } else {
+    auto load = [&](int tile, int set) {
+      load_k(tile, set);
+      load_v(tile, set);
+    };
+    auto store = [&](int tile, int stage, int set) {
+      store_k(smem + stage * STAGE, set);
+      store_v(tile, smem + stage * STAGE + KT * KP, set);
+    };
+    // Of the two waves of a SIMD one is preferred, so that they fall out of step: one's weights are worked out under the
+    // other's products. (Turns kept by barriers, with LDS read four products ahead, were no faster: 2190 us again
+    // at 16384 tokens, where the clock gives way to power.)
+    if (WQ == 8 && wave < 4) __builtin_amdgcn_s_setprio(1);
+    load(t0, 0);
+    if (SETS == 2) load(t0 + 1, SETS - 1);
+    __syncthreads();  // s_odd is 0
+    store(t0, 0, 0);
+    __syncthreads();
+    auto step = [&](int t, int h) __attribute__((always_inline)) {
+      load(t + SETS, SETS == 2 ? h : 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (wave_live && t * KT <= wmost) compute(t, h);
+      if (wave_live && t * KT <= wmost) {
+        scores(smem + h * STAGE);
+        weights(t);
+        values(smem + h * STAGE + KT * KP);
+      }
       __builtin_amdgcn_sched_barrier(0);
-      store(t + 1, h ^ 1, h ^ 1);
+      store(t + 1, h ^ 1, SETS == 2 ? h ^ 1 : 0);
       __syncthreads();
     };
-    int t = 0;
-    for (; t + 1 < ntiles; t += 2) {
+    int t = t0;
+    for (; t + 1 < t1; t += 2) {
       step(t, 0);
       step(t + 1, 1);
     }
-    if (t < ntiles) step(t, 0);
-  } else {
-    __syncthreads();
+    if (t < t1) step(t, 0);
   }
   if (!live) return;
   if (s_odd)
-    for (int j = max(all, 0) & ~(KT - 1); j <= lim; ++j) {
+    for (int j = max(max(all, 0) & ~(KT - 1), t0 * KT); j <= min(lim, t1 * KT - 1); ++j) {
       const T* x = reinterpret_cast<const T*>(a.v) + (long long)(k0 + j) * a.v_row + (long long)hk * a.v_head;
 #pragma unroll
       for (int i = 0; i < DB; ++i)
@@ -249,6 +313,20 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
     }
   l = swap_add(l);
+  if (a.splits > 1) {
+    const long long at = ((long long)(q0 + token) * a.HK * a.G + head) * a.splits + split;
+    if (half == 0) {
+      a.ml[2 * at] = m;
+      a.ml[2 * at + 1] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<f32x4*>(a.part + at * DP + 32 * i + 8 * k + 4 * half) =
+            (f32x4){o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]};
+    return;
+  }
   const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
   T* const out = reinterpret_cast<T*>(a.out) + (long long)(q0 + token) * a.out_row + (long long)head * a.out_head;
 #pragma unroll
@@ -263,31 +341,71 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
 }
 
+// out = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m) over the parts s of a query row's keys: one wave a row, 4 columns a
+// lane. Rows of no sequence stay.
+template <typename T, int DP>
+__global__ __launch_bounds__(BLOCK) void k_prompt_join(PromptDev a) {
+  const int lane = threadIdx.x % WAVE, H = a.HK * a.G;
+  const long long id = (long long)blockIdx.x * NWAVES + threadIdx.x / WAVE;
+  if (id >= (long long)a.q_rows * H) return;
+  const int row = (int)(id / H), head = (int)(id % H);
+  bool mine = false;
+  for (int b = lane; b < a.B; b += WAVE) {
+    int first;
+    const int n = packed(a.cu_q, b, a.q_rows, &first);
+    mine |= row >= first && row < first + n;
+  }
+  if (!__any(mine)) return;
+  float m = -__builtin_inff(), l = 0.f;
+  f32x4 v = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.ml[2 * (id * a.splits + s)]);
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  const int d = 4 * lane;
+  for (int s = 0; s < a.splits; ++s) {
+    const long long at = id * a.splits + s;
+    // not 0: an infinity that a row sees stays one, whatever it weighs
+    const float f = fmaxf(__builtin_amdgcn_exp2f(a.ml[2 * at] - base), 1.4e-45f);
+    l += a.ml[2 * at + 1] * f;
+    const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + at * DP + min(d, DP - 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i] * f;
+  }
+  if (d >= a.D) return;
+  T* out = reinterpret_cast<T*>(a.out) + (long long)row * a.out_row + (long long)head * a.out_head + d;
+  struct __attribute__((aligned(8))) { T e[4]; } w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.e[i] = (T)(l == 0.f ? 0.f : v[i] / l);
+  __builtin_memcpy(__builtin_assume_aligned(out, 8), &w, 8);
+}
+
 template <typename T, int DP, int WQ>
-pi_status launch_prompt_t(pi_ctx* c, PromptDev a) {
+pi_status launch_prompt_t(pi_ctx* c, const PromptDev& a) {
   constexpr size_t lds = prompt_lds<DP>();
   auto kern = k_prompt<T, DP, WQ>;
   PI_HIP(c, allow_lds(kern, lds));
-  // every sequence's last tile may be a part of one
-  a.tiles = (int)(((long long)a.q_rows * a.G + 32 * WQ - 1) / (32 * WQ)) + a.B - 1;
-  PI_HIP(c, launch_kb(c, 0, kern, dim3((unsigned)(a.tiles * a.HK)), 64 * WQ, lds, a));
+  PI_HIP(c, launch_kb(c, 0, kern, dim3((unsigned)(a.tiles * a.HK * a.splits)), 64 * WQ, lds, a));
+  if (a.splits > 1) {
+    const long long rows = (long long)a.q_rows * a.HK * a.G;
+    PI_HIP(c, launch_k(c, 0, k_prompt_join<T, DP>, dim3((unsigned)((rows + NWAVES - 1) / NWAVES)), 0, a));
+  }
   return PI_OK;
 }
 
-// Four waves where sequences are short: a tile of eight would be mostly empty.
 template <typename T, int DP>
-pi_status launch_prompt_d(pi_ctx* c, const PromptDev& a) {
-  if (DP <= 128 && (long long)a.q_rows * a.G <= 128ll * a.B) return launch_prompt_t<T, DP, DP <= 128 ? 4 : 8>(c, a);
+pi_status launch_prompt_d(pi_ctx* c, const PromptDev& a, int wq) {
+  if constexpr (DP <= 128) {
+    if (wq == 4) return launch_prompt_t<T, DP, 4>(c, a);
+  }
   return launch_prompt_t<T, DP, 8>(c, a);
 }
 
 template <typename T>
-pi_status launch_prompt(pi_ctx* c, const PromptDev& a) {
+pi_status launch_prompt(pi_ctx* c, const PromptDev& a, int wq) {
   switch (padded_dim_p(a.D)) {
-    case 64: return launch_prompt_d<T, 64>(c, a);
-    case 96: return launch_prompt_d<T, 96>(c, a);
-    case 128: return launch_prompt_d<T, 128>(c, a);
-    default: return launch_prompt_d<T, 256>(c, a);
+    case 64: return launch_prompt_d<T, 64>(c, a, wq);
+    case 96: return launch_prompt_d<T, 96>(c, a, wq);
+    case 128: return launch_prompt_d<T, 128>(c, a, wq);
+    default: return launch_prompt_d<T, 256>(c, a, wq);
   }
 }
 
@@ -309,8 +427,25 @@ pi_status pi_prompt_create(pi_ctx* ctx, int32_t dtype, int32_t heads, int32_t kv
   // row numbers of a head's group, and workgroups, are 32-bit numbers
   if (((int64_t)max_tokens + 256ll * max_batch) * heads >= 1ll << 30)
     return fail(ctx, PI_ERR_UNSUPPORTED, "%d tokens of %d sequences and %d heads are too many", max_tokens, max_batch, heads);
-  pi_prompt* p = new (std::nothrow) pi_prompt{ctx, dtype, heads, kv_heads, head_dim, max_tokens, max_batch, scale};
-  if (p == nullptr) return fail(ctx, PI_ERR_OOM, "host allocation failed");
+  // scratch of the largest call whose keys are split, of however many rows
+  const int HK = kv_heads, G = heads / kv_heads, DP = padded_dim_p(head_dim);
+  size_t rows = 0;
+  for (int64_t n = 1; n <= max_tokens; n += std::max<int64_t>(1, n / 64)) {
+    const int64_t next = std::min<int64_t>(max_tokens, n + std::max<int64_t>(1, n / 64) - 1);
+    const PromptPlan q = prompt_plan(ctx->cus, HK, G, DP, (int)n, 1, INT64_MAX);
+    if (q.splits > 1) rows = std::max(rows, (size_t)next * heads * q.splits);
+  }
+  PI_HIP(ctx, hipSetDevice(ctx->device));
+  uint8_t* ws = nullptr;
+  if (rows > 0 && hipMalloc(reinterpret_cast<void**>(&ws), rows * (DP + 2) * 4) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(ctx, PI_ERR_OOM, "prompt attention scratch of %zu bytes", rows * (DP + 2) * 4);
+  }
+  pi_prompt* p = new (std::nothrow) pi_prompt{ctx, dtype, heads, kv_heads, head_dim, max_tokens, max_batch, scale, ws, rows};
+  if (p == nullptr) {
+    (void)hipFree(ws);
+    return fail(ctx, PI_ERR_OOM, "host allocation failed");
+  }
   ctx_retain(ctx);
   *out = p;
   return PI_OK;
@@ -318,6 +453,8 @@ pi_status pi_prompt_create(pi_ctx* ctx, int32_t dtype, int32_t heads, int32_t kv
 
 void pi_prompt_destroy(pi_prompt* p) {
   if (p == nullptr) return;
+  (void)hipSetDevice(p->ctx->device);
+  (void)hipFree(p->ws);
   ctx_release(p->ctx);
   delete p;
 }
@@ -336,16 +473,23 @@ pi_status pi_prompt_attention(pi_ctx* ctx, pi_prompt* prompt, const pi_prompt_ar
   if (a.q_rows == 0) return PI_OK;
   PI_TRY(check_bnh(ctx, "q", a.q, 0, a.q_row, a.q_head));
   PI_TRY(check_bnh(ctx, "out", a.out, 0, a.out_row, a.out_head));
+  if (a.k_row < 0 || a.v_row < 0 || a.k_row >= 1 << 24 || a.v_row >= 1 << 24)
+    return fail(ctx, PI_ERR_UNSUPPORTED, "rows of k and v are less than 2^24 elements apart");
   if (a.k_rows > 0) {
     PI_TRY(check_bnh(ctx, "k", a.k, 0, a.k_row, a.k_head));
     PI_TRY(check_bnh(ctx, "v", a.v, 0, a.v_row, a.v_head));
   }
   PI_HIP(ctx, hipSetDevice(ctx->device));
+  const int HK = prompt->kv_heads, G = prompt->heads / HK, DP = padded_dim_p(prompt->head_dim);
+  PromptPlan p = prompt_plan(ctx->cus, HK, G, DP, a.q_rows, a.B, a.k_rows);
+  const int64_t rows = (int64_t)a.q_rows * prompt->heads;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.splits, (int64_t)prompt->ws_rows / rows));
+  float* part = reinterpret_cast<float*>(prompt->ws);
   const PromptDev d{static_cast<const uint8_t*>(a.q), static_cast<const uint8_t*>(a.k), static_cast<const uint8_t*>(a.v),
                     static_cast<uint8_t*>(a.out), a.cu_q, a.cu_k != nullptr ? a.cu_k : a.cu_q, a.q_row, a.q_head, a.k_row,
-                    a.k_head, a.v_row, a.v_head, a.out_row, a.out_head, a.B, a.q_rows, a.k_rows, prompt->kv_heads,
-                    prompt->heads / prompt->kv_heads, prompt->head_dim, 0, prompt->scale * 1.4426950408889634f};
-  return prompt->dtype == PI_T_F16 ? launch_prompt<half_t>(ctx, d) : launch_prompt<bf16_t>(ctx, d);
+                    a.k_head, a.v_row, a.v_head, a.out_row, a.out_head, part, part + prompt->ws_rows * DP, a.B, a.q_rows,
+                    a.k_rows, HK, G, prompt->head_dim, p.tiles, p.splits, prompt->scale * 1.4426950408889634f};
+  return prompt->dtype == PI_T_F16 ? launch_prompt<half_t>(ctx, d, p.wq) : launch_prompt<bf16_t>(ctx, d, p.wq);
 }
 
 }  // extern "C"

@@ -540,6 +540,7 @@ void pi_prompt_destroy(pi_prompt *prompt);
 /*   q, out     [q_rows][heads][head_dim];  k, v [k_rows][kv_heads][head_dim]
  *   cu_q, cu_k device int32 [B+1], ascending, cu_k NULL: cu_q; offsets are taken into [0, q_rows] and
  *              [0, k_rows]
+ *   k_row, v_row  below 2^24
  *   out may not share memory with q, k or v */
 typedef struct pi_prompt_args {
   const void *q;
