@@ -425,7 +425,7 @@ pi_status pi_prompt_create(pi_ctx* ctx, int32_t dtype, int32_t heads, int32_t kv
   if (max_tokens < 1 || max_batch < 1) return fail(ctx, PI_ERR_INVALID, "bad limits: %d tokens, %d sequences", max_tokens, max_batch);
   if (!(scale > 0.f) || scale > 3e38f) return fail(ctx, PI_ERR_INVALID, "scale must be finite and above 0");
   // row numbers of a head's group, and workgroups, are 32-bit numbers
-  if (((int64_t)max_tokens + 256ll * max_batch) * heads >= 1ll << 30)
+  if (((int64_t)max_tokens + 256ll * max_batch) * heads >= 1ll << 29)
     return fail(ctx, PI_ERR_UNSUPPORTED, "%d tokens of %d sequences and %d heads are too many", max_tokens, max_batch, heads);
   // scratch of the largest call whose keys are split, of however many rows
   const int HK = kv_heads, G = heads / kv_heads, DP = padded_dim_p(head_dim);
@@ -473,7 +473,7 @@ pi_status pi_prompt_attention(pi_ctx* ctx, pi_prompt* prompt, const pi_prompt_ar
   if (a.q_rows == 0) return PI_OK;
   PI_TRY(check_bnh(ctx, "q", a.q, 0, a.q_row, a.q_head));
   PI_TRY(check_bnh(ctx, "out", a.out, 0, a.out_row, a.out_head));
-  if (a.k_row < 0 || a.v_row < 0 || a.k_row >= 1 << 24 || a.v_row >= 1 << 24)
+  if (a.k_rows > 1 && (a.k_row < 0 || a.v_row < 0 || a.k_row >= 1 << 24 || a.v_row >= 1 << 24))
     return fail(ctx, PI_ERR_UNSUPPORTED, "rows of k and v are less than 2^24 elements apart");
   if (a.k_rows > 0) {
     PI_TRY(check_bnh(ctx, "k", a.k, 0, a.k_row, a.k_head));
