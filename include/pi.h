@@ -294,7 +294,7 @@ pi_status pi_permute_rows(pi_ctx *ctx, const void *src, void *dst, const int32_t
  * packed prompts, and the cache held in 4 bits.
  * They follow the conventions above. Tensors of these calls may be views: strides are given
  * in elements, the last axis is contiguous, and rows start at a multiple of 16 bytes unless a
- * call says otherwise. A pi_attn and a pi_verifier keep their own scratch, sized when they are
+ * call says otherwise. A pi_attn, a pi_prompt and a pi_verifier keep their own scratch, sized when they are
  * created. The product's scratch is the context's, one buffer of 33.5 MB that all its pi_linear
  * share: as for the FFN's calls, they and the replays of graphs that hold them must be ordered.
  * Every handle borrows the pointers of its description; a pi_attn keeps its cache's description
@@ -384,7 +384,7 @@ pi_status pi_kv_append(pi_ctx *ctx, const pi_kv *kv, const pi_append_args *args)
  *   cu         device int32 [B+1], ascending; rows outside [0, rows) are not written
  *   start      device int32 [B] (negative: 0), or NULL: 0
  *   ctx_len    device int32 [B], taken as 0 below 0 and as the table's positions above them
- *   k_out, v_out  [rows][heads][head_dim] of the cache's dtype, strides for both */
+ *   k_out, v_out  [rows][heads][head_dim] of the cache's dtype, strides for both; rows up to 2^27 */
 typedef struct pi_read_args {
   const int32_t *table;
   int64_t table_stride;
@@ -405,7 +405,8 @@ pi_status pi_kv_read(pi_ctx *ctx, const pi_kv *kv, const pi_read_args *args);
  * values, the new nodes' are given in its dtype.
  *   heads      query heads, a multiple of the cache's heads
  *   scale      finite, above 0
- *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch */
+ *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch
+ * Over a 4-bit cache B times the table's positions is below 2^37. */
 pi_status pi_attn_create(pi_ctx *ctx, const pi_kv *kv, int32_t heads, int32_t max_batch, int32_t max_nodes,
                          float scale, pi_attn **out);
 void pi_attn_destroy(pi_attn *attn);
@@ -564,11 +565,12 @@ pi_status pi_prompt_attention(pi_ctx *ctx, pi_prompt *prompt, const pi_prompt_ar
  * Pair i is elements i and i + rot/2, or 2i and 2i + 1 where `interleaved`. Angles are formed and
  * reduced in 64 bits, everything else is in fp32, rounded once.
  *   q, k       [T][heads][head_dim] and [T][kv_heads][head_dim] of x_dtype; heads or kv_heads may be 0
- *              (q or k is not looked at); head_dim a multiple of 8 up to 512
+ *              (q or k is not looked at); head_dim a multiple of 8 up to 512; T up to 2^23
  *   q_out, k_out  of y_dtype; each may be its input itself, of the same type and strides
  *   q_w, k_w   fp32 [head_dim], or NULL: no norm of these heads
  *   pos        device int32 [T];  inv_freq device fp32 [rot/2]
- *   rot        a multiple of 4 up to head_dim, or 0: no rotation (pos and inv_freq are not looked at) */
+ *   rot        a multiple of 4 up to head_dim (of 8 where heads are above 256), or 0: no rotation (pos and
+ *              inv_freq are not looked at) */
 typedef struct pi_rope_args {
   const void *q, *k;
   int64_t q_row, q_head, k_row, k_head;
