@@ -17,7 +17,13 @@ using namespace pi;
 namespace {
 
 constexpr int KT4 = 64;  // keys of a tile
-constexpr float SHIFT4 = 14.f;  // weights are carried times 2^14, as over a plain fp16 cache
+constexpr float SHIFT4 = 14.f;  // weights of cached tiles are carried times 2^14, as over a plain fp16 cache
+// New nodes in bf16 may hold values up to fp32's end: after the cached tiles the sums go on times 2^-8, so that 64 of them
+// with weights up to 1 stay in range. Where nodes are fp16, the 2^14 stays. A factor of 2^-22 loses nothing of the cached
+// tiles' sums: a weight that fp16 holds is 2^-38 or more of the largest, a cached value 0 or 2^-24 or more.
+template <typename T> constexpr float SHIFT_NEW = __is_same(T, half_t) ? SHIFT4 : -8.f;
+template <typename T> constexpr float CACHED_TO_NEW = __is_same(T, half_t) ? 1.f : 0x1p-22f;
+static_assert(SHIFT_NEW<bf16_t> - SHIFT4 == -22.f, "the factor between the two");
 
 // Elements 4w..4w+3 and 16+4w..+3 of a block, at p and 32 bytes on.
 __device__ __forceinline__ u32x4 two_pieces(const uint8_t* p) {
@@ -256,7 +262,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
   float m = -__builtin_inff(), l = 0.f;  // running maximum (log2 domain); this half's sum
 
   // One tile. `seen` (bit j: key j) counts where `masked`.
-  auto compute = [&](auto type, int stage, float scale2, bool masked, uint64_t seen) __attribute__((always_inline)) {
+  auto compute = [&](auto type, int stage, float scale2, float shift, bool masked, uint64_t seen) __attribute__((always_inline)) {
     typedef decltype(type) M;
     typedef typename Mm<M>::v8 v8;
     const uint8_t* kb0 = smem + stage * STAGE;
@@ -301,7 +307,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], scale2, SHIFT4 - base));
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], scale2, shift - base));
         l += w;
         pf[kb][r >> 3][r & 7] = (M)w;
       }
@@ -335,7 +341,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
       load(t + 2, h);
       __builtin_amdgcn_sched_barrier(0);
       const int left = -tile_from_end<KT>(t, len);
-      if (wave_live) compute(half_t(), h, scale_c, left < KT, left < KT ? (1ull << left) - 1 : 0);
+      if (wave_live) compute(half_t(), h, scale_c, SHIFT4, left < KT, left < KT ? (1ull << left) - 1 : 0);
       __builtin_amdgcn_sched_barrier(0);
       store(h ^ 1, h ^ 1);
       __syncthreads();
@@ -346,6 +352,13 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
       step(t + 1, 1);
     }
     if (t < cend) step(t, 0);
+  }
+  if constexpr (CACHED_TO_NEW<T> != 1.f) {
+    l *= CACHED_TO_NEW<T>;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] *= CACHED_TO_NEW<T>;
   }
   if (t1 > new_tile) {
     __syncthreads();  // s_odd is 0
@@ -374,7 +387,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
     if constexpr (!__is_same(T, half_t)) load_q();
     uint64_t seen = a.tree != nullptr ? a.tree[(long long)b * a.N + node] : (2ull << node) - 1;
     if (a.N < 64) seen &= (1ull << a.N) - 1;
-    if (wave_live) compute(T(), 0, a.scale2, true, seen);
+    if (wave_live) compute(T(), 0, a.scale2, SHIFT_NEW<T>, true, seen);
     if (s_odd && live)
       for (int j = 0; j < a.N; ++j)
         if ((seen >> j) & 1) {
@@ -600,7 +613,7 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
   const uint8_t* const vl = vt + (4 * g + (c16 >> 2)) * VP + 8 * (c16 & 3);
 
   // s[q][t]: scores of keys 16t + 4g + 0..3 and row 16q + c16
-  auto weigh = [&](auto type, f32x4 (&s)[NQ][2], const float (&scale2)[NQ]) __attribute__((always_inline)) {
+  auto weigh = [&](auto type, f32x4 (&s)[NQ][2], const float (&scale2)[NQ], float shift) __attribute__((always_inline)) {
     typedef decltype(type) M;
     typedef M m8 __attribute__((ext_vector_type(8)));
     u32x4 pf[NQ];
@@ -624,7 +637,7 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
       m8 p;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q][r >> 2][r & 3], scale2[q], SHIFT4 - base));
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q][r >> 2][r & 3], scale2[q], shift - base));
         l[q] += w;
         p[r] = (M)w;
       }
@@ -673,7 +686,7 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
       for (int q = 0; q < NQ; ++q) hide(s, q, left <= 0 ? 0u : (1u << left) - 1);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    weigh(half_t(), s, scale_c);
+    weigh(half_t(), s, scale_c, SHIFT4);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
   if (t0 < cend) {
@@ -683,6 +696,16 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
       step(t + 1, 1);
     }
     if (t < cend) step(t, 0);
+  }
+  if constexpr (CACHED_TO_NEW<T> != 1.f) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      l[q] *= CACHED_TO_NEW<T>;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[q][i][r] *= CACHED_TO_NEW<T>;
+    }
   }
   if (t1 > new_tile && wave == 0) {
     // the new nodes (N <= R <= 32), one a lane and key tile, in the order of the positions
@@ -726,7 +749,7 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
       scale_n[q] = a.scale2;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    weigh(T(), s, scale_n);
+    weigh(T(), s, scale_n, SHIFT_NEW<T>);
     if (__any(odd))
 #pragma unroll
       for (int q = 0; q < NQ; ++q)

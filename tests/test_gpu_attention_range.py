@@ -1,0 +1,58 @@
+"""Attention of values near the end of bf16's range: a mean of values is no larger than the largest of them, so that its
+parts may not leave fp32 on the way. Tolerances are those of the operators' other tests, relative to the values."""
+import random
+
+import pytest
+import torch
+
+from tests.test_gpu_decoder import sees_of, trees, words_of
+from tests.test_gpu_prompts import BF16, check_attention4, make_cache4, run_attention4
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import activation_sparse_ffn_layer_amd as pi
+
+MAX = torch.finfo(BF16).max
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return pi.Context(max_batch=1, max_d=64, max_ffn=64, max_rank=0)
+
+
+def far_values(g, *shape):
+    """bf16 values of either sign up to the largest one, a quarter of them the largest itself."""
+    x = (2 * torch.rand(*shape, generator=g) - 1) * MAX
+    return torch.where(torch.rand(*shape, generator=g) < 0.25, MAX, x).to(BF16)
+
+
+@pytest.mark.parametrize("B,N,G,D,lens", [
+    (1, 1, 1, 64, [0]),
+    (2, 3, 2, 96, [40, 0]),             # rows of a few waves
+    (1, 28, 1, 128, [300]),
+    (1, 30, 2, 128, [0]),               # a row tile of four waves
+    (2, 64, 4, 64, [5, 200]),           # of eight
+    (1, 64, 1, 256, [130]),
+])
+def test_new_values_over_4_bits(ctx, B, N, G, D, lens):
+    HK = 2
+    g = torch.Generator().manual_seed(31)
+    parts, table = make_cache4(lens, max(lens) + N, HK, D, 16, 32, dtype=BF16)
+    q = torch.randn(B, N, HK * G, D, generator=g).to(BF16)
+    kn = torch.randn(B, N, HK, D, generator=g).to(BF16)
+    vn = far_values(g, B, N, HK, D)
+    sees = sees_of(trees(random.Random(5), B, N, 3))
+    out = run_attention4(ctx, q, parts, kn, vn, words_of(sees), table, lens, D ** -0.5)
+    check_attention4(out, q, parts, kn, vn, sees, table, lens, D ** -0.5)
+
+
+@pytest.mark.parametrize("N,G", [(32, 1), (64, 1), (64, 8)])
+def test_the_largest_value_of_every_new_node_over_4_bits(ctx, N, G):
+    """Equal weights and equal values: the value itself."""
+    D = 64
+    parts, table = make_cache4([0], N, 1, D, 16, 33)
+    q = torch.zeros(1, N, G, D, dtype=BF16)
+    vn = torch.full((1, N, 1, D), MAX, dtype=BF16)
+    out = run_attention4(ctx, q, parts, vn, vn, None, table, [0], 1.0)
+    assert (out == MAX).all()
