@@ -64,6 +64,10 @@ struct PromptDev {
 
 constexpr int PKT = 64;  // keys of a tile
 
+// The power of two that weights carry. In bf16 values go up to fp32's end: 2^30 weights of at most 2^-31 keep their sum in
+// range, and weights down to 2^-95 of the largest stay normal numbers. fp16: as over a plain cache.
+template <typename T> constexpr float PROMPT_SHIFT = __is_same(T, half_t) ? Mm<half_t>::SHIFT : -31.f;
+
 // Sequence b's part of `rows` packed rows: from *first on, the number of rows is returned.
 __device__ __forceinline__ int packed(const int32_t* cu, int b, int rows, int* first) {
   const int f = min(max(cu[b], 0), rows);
@@ -240,7 +244,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], a.scale2, Mm<T>::SHIFT - base));
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], a.scale2, PROMPT_SHIFT<T> - base));
         l += w;
         pf[kb][r >> 3][r & 7] = (T)w;
       }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests.test_gpu_decoder import sees_of, trees, words_of
-from tests.test_gpu_prompts import BF16, check_attention4, make_cache4, run_attention4
+from tests.test_gpu_prompts import BF16, check_attention4, check_prompt, make_cache4, offsets, run_attention4, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,26 @@ def test_the_largest_value_of_every_new_node_over_4_bits(ctx, N, G):
     vn = torch.full((1, N, 1, D), MAX, dtype=BF16)
     out = run_attention4(ctx, q, parts, vn, vn, None, table, [0], 1.0)
     assert (out == MAX).all()
+
+
+@pytest.mark.parametrize("H,HK,D,seqs", [
+    (4, 2, 64, [(70, 0), (1, 100)]),
+    (2, 2, 256, [(65, 30)]),
+    (8, 2, 128, [(9, 2500)]),           # keys cut into parts
+    (1, 1, 40, [(3, 0), (200, 7)]),
+])
+def test_prompt_values(ctx, H, HK, D, seqs):
+    g = torch.Generator().manual_seed(34)
+    cu_q, cu_k = offsets([n for n, _ in seqs]), offsets([n + h for n, h in seqs])
+    q = torch.randn(cu_q[-1], H, D, generator=g).to(BF16)
+    k, v = torch.randn(cu_k[-1], HK, D, generator=g).to(BF16), far_values(g, cu_k[-1], HK, D)
+    out = run_prompt(ctx, q, k, v, cu_q, cu_k, D ** -0.5)
+    check_prompt(out, q, k, v, cu_q, cu_k, D ** -0.5)
+
+
+@pytest.mark.parametrize("n,held", [(130, 0), (2, 4000)])
+def test_the_largest_value_of_every_key_of_a_prompt(ctx, n, held):
+    """Equal weights and equal values: the value itself."""
+    q = torch.zeros(n, 2, 64, dtype=BF16)
+    v = torch.full((n + held, 1, 64), MAX, dtype=BF16)
+    assert (run_prompt(ctx, q, v, v, [0, n], [0, n + held], 1.0) == MAX).all()
