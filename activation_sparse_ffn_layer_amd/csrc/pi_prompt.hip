@@ -298,7 +298,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
         values(smem + h * STAGE + KT * KP);
       }
       __builtin_amdgcn_sched_barrier(0);
-      store(t + 1, h ^ 1, SETS == 2 ? h ^ 1 : 0);
+      if (t + 1 < t1) store(t + 1, h ^ 1, SETS == 2 ? h ^ 1 : 0);  // past the last tile nothing was loaded
       __syncthreads();
     };
     int t = t0;
