@@ -29,6 +29,9 @@ struct pi_prompt {
 namespace {
 
 constexpr int SPLITS = 32;  // at most
+// Workgroups that the cutting of keys may launch: the last row tiles of many sequences are each launched for every part,
+// and a launch has fewer than 2^32 threads.
+constexpr int64_t SPLIT_WGS = 1 << 20;
 
 // How a call is cut. Eight waves a workgroup where their row tiles fill the chip, else four: more workgroups, and tiles that
 // fit short sequences (500 tokens of 32 heads: 21 us, with eight 26; with two, whose threads have too many rows to load,
@@ -46,10 +49,10 @@ PromptPlan prompt_plan(int cus, int HK, int G, int DP, int rows, int B, int64_t 
     if (DP > 128 || p.wq == 4 || (r / (32 * p.wq) * HK >= cus && r > 128ll * B)) break;
   }
   const int64_t full = std::max<int64_t>(1, (r + 32 * p.wq - 1) / (32 * p.wq)) * HK;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({SPLITS, (p.wq == 8 ? 1 : 2) * cus / full, keys / B / (4 * 64)}));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({SPLITS, (p.wq == 8 ? 1 : 2) * cus / full, keys / B / (4 * 64),
+                                                          SPLIT_WGS / ((int64_t)p.tiles * HK)}));
   return p;
 }
-
 
 struct PromptDev {
   const uint8_t *q, *k, *v;

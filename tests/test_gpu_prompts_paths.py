@@ -92,3 +92,20 @@ def test_keys_in_parts(ctx, D, dtype):
     assert not odd[:6, 2:, 2].isfinite().any()
     odd[:6, 2:, 2] = out[:6, 2:, 2]
     assert torch.equal(odd, out)
+
+
+def test_one_query_among_many_empty_sequences(ctx):
+    """Few rows of many sequences: each part of the keys is launched for every sequence's row tile, which may not pass
+    the threads of a launch (35000 * 16 heads * 32 parts * 256). All rows of keys are one, repeated."""
+    B, HK, D = 35000, 16, 8
+    g = torch.Generator(DEV).manual_seed(44)
+    q = torch.randn(1, HK, D, generator=g, device=DEV).to(F16)
+    k, v = (torch.randn(1, HK, D, generator=g, device=DEV).to(F16).expand(B << 13, HK, D) for _ in range(2))
+    prompt = pi.PromptAttn(ctx, HK, HK, D, F16, 1, B, 0.5)
+    cu_q, cu_k = (torch.zeros(B + 1, dtype=torch.int32, device=DEV) for _ in range(2))
+    cu_q[-1], cu_k[-1] = 1, 3000
+    out = torch.full_like(q, NAN)
+    pi.prompt_attention(ctx, prompt, q, k, v, cu_q, cu_k, out)
+    torch.cuda.synchronize()
+    # equal weights (fp16's largest power of two below 2^15 is exact) of equal values
+    assert ((out.double() - v[:1].double()).abs() <= 2.0 ** -11 * v[:1].double().abs() + 3000 * f * v[:1].double().abs()).all()
