@@ -511,7 +511,8 @@ pi_status pi_attn_create(pi_ctx* ctx, const pi_kv* kv, int32_t heads, int32_t ma
     return fail(ctx, PI_ERR_INVALID, "%d query heads are no multiple of the cache's %d", heads, kv->desc.heads);
   if (max_batch < 1 || max_nodes < 1) return fail(ctx, PI_ERR_INVALID, "bad limits: %d sequences, %d nodes", max_batch, max_nodes);
   if (max_nodes > 64) return fail(ctx, PI_ERR_UNSUPPORTED, "%d nodes: a tree has at most 64", max_nodes);
-  if (!(scale > 0.f) || scale > 3e38f) return fail(ctx, PI_ERR_INVALID, "scale must be finite and above 0");
+  // what the kernels use is its product with log2(e)
+  if (!(scale > 0.f) || scale > 0x1p127f) return fail(ctx, PI_ERR_INVALID, "scale must be above 0 and at most 2^127");
   const int HK = kv->desc.heads, G = heads / HK;
   const int DP = kv->q4 ? padded_dim4(kv->desc.head_dim) : padded_dim(kv->desc.head_dim);
   if ((int64_t)max_batch * max_nodes * heads >= (1ll << 31) / 64)

@@ -435,7 +435,8 @@ pi_status pi_prompt_create(pi_ctx* ctx, int32_t dtype, int32_t heads, int32_t kv
   if (head_dim < 8 || head_dim % 8) return fail(ctx, PI_ERR_INVALID, "head_dim must be a multiple of 8 (got %d)", head_dim);
   if (head_dim > 256) return fail(ctx, PI_ERR_UNSUPPORTED, "head_dim %d above 256", head_dim);
   if (max_tokens < 1 || max_batch < 1) return fail(ctx, PI_ERR_INVALID, "bad limits: %d tokens, %d sequences", max_tokens, max_batch);
-  if (!(scale > 0.f) || scale > 3e38f) return fail(ctx, PI_ERR_INVALID, "scale must be finite and above 0");
+  // what the kernels use is its product with log2(e)
+  if (!(scale > 0.f) || scale > 0x1p127f) return fail(ctx, PI_ERR_INVALID, "scale must be above 0 and at most 2^127");
   // row numbers of a head's group, and workgroups, are 32-bit numbers
   if (((int64_t)max_tokens + 256ll * max_batch) * heads >= 1ll << 29)
     return fail(ctx, PI_ERR_UNSUPPORTED, "%d tokens of %d sequences and %d heads are too many", max_tokens, max_batch, heads);

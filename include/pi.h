@@ -404,7 +404,7 @@ pi_status pi_kv_read(pi_ctx *ctx, const pi_kv *kv, const pi_read_args *args);
  * seen does not enter the result, whatever it holds. Over a 4-bit cache the cached keys and values are its
  * values, the new nodes' are given in its dtype.
  *   heads      query heads, a multiple of the cache's heads
- *   scale      finite, above 0
+ *   scale      above 0, at most 2^127
  *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch
  * Over a 4-bit cache B times the table's positions is below 2^37. */
 pi_status pi_attn_create(pi_ctx *ctx, const pi_kv *kv, int32_t heads, int32_t max_batch, int32_t max_nodes,
@@ -530,7 +530,7 @@ pi_status pi_linear_q8(pi_ctx *ctx, pi_linear *lin, const int8_t *x, int64_t x_s
  * seen does not enter the result, whatever it holds. Rows of no sequence stay as they are. The handle
  * keeps its own scratch: calls that share it, and the replays of graphs that hold them, are ordered.
  *   heads      a multiple of kv_heads;  head_dim a multiple of 8 up to 256
- *   dtype      PI_T_F16 or PI_T_BF16;  scale finite, above 0
+ *   dtype      PI_T_F16 or PI_T_BF16;  scale above 0, at most 2^127
  *   max_tokens, max_batch   limits of rows of q and of sequences */
 typedef struct pi_prompt pi_prompt;
 

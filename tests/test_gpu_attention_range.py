@@ -79,3 +79,24 @@ def test_the_largest_value_of_every_key_of_a_prompt(ctx, n, held):
     q = torch.zeros(n, 2, 64, dtype=BF16)
     v = torch.full((n + held, 1, 64), MAX, dtype=BF16)
     assert (run_prompt(ctx, q, v, v, [0, n], [0, n + held], 1.0) == MAX).all()
+
+
+def test_scales_whose_logarithm_leaves_the_range(ctx):
+    """The kernels use scale times log2(e): up to 2^127 it is a number, and keys of zeros weigh alike."""
+    parts, table = make_cache4([20], 22, 1, 64, 16, 35)
+    plain = pi.KvCache(ctx, *[torch.zeros(2, 16, 1, 64, dtype=BF16, device="cuda")] * 2)
+    codes, scales = (torch.zeros(2, 16, 1, n, dtype=t, device="cuda") for n, t in ((32, torch.uint8), (2, torch.float16)))
+    for scale in (2.9e38, 1.71e38):
+        with pytest.raises(pi.PiError, match="scale"):
+            pi.PromptAttn(ctx, 2, 1, 64, BF16, 8, 1, scale)
+        for cache in (plain, pi.KvCache4(ctx, codes, codes, scales, scales, BF16)):
+            with pytest.raises(pi.PiError, match="scale"):
+                pi.Attn(ctx, cache, 2, 1, 1, scale)
+    g = torch.Generator().manual_seed(36)
+    q, v = torch.randn(9, 2, 64, generator=g).to(BF16), torch.randn(9, 1, 64, generator=g).to(BF16)
+    k = torch.zeros_like(v)
+    check_prompt(run_prompt(ctx, q, k, v, [0, 9], None, 2.0 ** 127), q, k, v, [0, 9], [0, 9], 2.0 ** 127)
+    parts[1].zero_()  # keys: their scales
+    kn, vn, sees = (t[None, :2] for t in (k, v, torch.ones(2, 2, dtype=torch.bool).tril()))
+    out = run_attention4(ctx, q[None, :2], parts, kn, vn, None, table, [20], 2.0 ** 127)
+    check_attention4(out, q[None, :2], parts, kn, vn, sees, table, [20], 2.0 ** 127)
