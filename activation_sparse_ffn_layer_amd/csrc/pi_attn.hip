@@ -374,7 +374,7 @@ __global__ __launch_bounds__(64 * WQ * WK) __attribute__((amdgpu_waves_per_eu(2,
               (long long)(hk * a.G + r % a.G) * a.out_head + d;
       struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w.e[i] = (T)(ll == 0.f ? 0.f : v[i] * inv);
+      for (int i = 0; i < 4; ++i) w.e[i] = mean_out<T>(ll == 0.f ? 0.f : v[i] * inv, v[i]);
       __builtin_memcpy(__builtin_assume_aligned(o4, 8), &w, 8);
     } else {
       const long long at = ((long long)slot * a.HK + hk) * a.R + r;

@@ -51,6 +51,15 @@ template <> struct Mm<bf16_t> {
   }
 };
 
+// The mean `x` of values whose weighted sum is `sum`. Values that are numbers have no larger mean, but their weights' rounding
+// may bring it past the type's largest number, where the conversion gives an infinity.
+template <typename T>
+__device__ __forceinline__ T mean_out(float x, float sum) {
+  constexpr float TOP = __is_same(T, half_t) ? 65504.f : 0x1.FEp127f;
+  if (fabsf(sum) < __builtin_inff()) x = x > TOP ? TOP : x < -TOP ? -TOP : x;
+  return (T)x;
+}
+
 __device__ __forceinline__ int acc_row(int r, int half) { return 8 * (r >> 2) + 4 * half + (r & 3); }
 
 // The other half's value of v (lane ^ 32).
@@ -194,7 +203,7 @@ __device__ __forceinline__ void join_parts(const AttnDev& a, int b, int hk, int 
          (long long)(hk * a.G + r % a.G) * a.out_head + d;
   struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w.e[i] = (T)(l == 0.f ? 0.f : v[i] / l);
+  for (int i = 0; i < 4; ++i) w.e[i] = mean_out<T>(l == 0.f ? 0.f : v[i] / l, v[i]);
   __builtin_memcpy(__builtin_assume_aligned(o, 8), &w, 8);
 }
 

@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
       if (direct) {
         struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w.e[e] = (T)(l == 0.f ? 0.f : v[e] * inv);
+        for (int e = 0; e < 4; ++e) w.e[e] = mean_out<T>(l == 0.f ? 0.f : v[e] * inv, v[e]);
         __builtin_memcpy(__builtin_assume_aligned(out + d, 8), &w, 8);
       } else {
         *reinterpret_cast<f32x4*>(a.part + at * DP + d) = v;
@@ -820,7 +820,7 @@ void k_attn4_few(AttnDev a, Kv4Dev sc) {
                (long long)(hk * a.G + r % a.G) * a.out_head + d;
       struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w.e[e] = (T)(lt == 0.f ? 0.f : v[e] * inv);
+      for (int e = 0; e < 4; ++e) w.e[e] = mean_out<T>(lt == 0.f ? 0.f : v[e] * inv, v[e]);
       __builtin_memcpy(__builtin_assume_aligned(out, 8), &w, 8);
     } else {
       const long long at = ((long long)(span + b) * a.HK + hk) * a.R + r;

@@ -348,7 +348,7 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
       const int d = 32 * i + 8 * k + 4 * half;
       struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w.e[e] = (T)(l == 0.f ? 0.f : o[i][4 * k + e] * inv);
+      for (int e = 0; e < 4; ++e) w.e[e] = mean_out<T>(l == 0.f ? 0.f : o[i][4 * k + e] * inv, o[i][4 * k + e]);
       if (d < a.D) __builtin_memcpy(__builtin_assume_aligned(out + d, 8), &w, 8);
     }
 }
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(BLOCK) void k_prompt_join(PromptDev a) {
   T* out = reinterpret_cast<T*>(a.out) + (long long)row * a.out_row + (long long)head * a.out_head + d;
   struct __attribute__((aligned(8))) { T e[4]; } w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w.e[i] = (T)(l == 0.f ? 0.f : v[i] / l);
+  for (int i = 0; i < 4; ++i) w.e[i] = mean_out<T>(l == 0.f ? 0.f : v[i] / l, v[i]);
   __builtin_memcpy(__builtin_assume_aligned(out, 8), &w, 8);
 }
 

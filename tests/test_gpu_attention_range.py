@@ -1,11 +1,12 @@
 """Attention of values near the end of bf16's range: a mean of values is no larger than the largest of them, so that its
 parts may not leave fp32 on the way. Tolerances are those of the operators' other tests, relative to the values."""
+import math
 import random
 
 import pytest
 import torch
 
-from tests.test_gpu_decoder import sees_of, trees, words_of
+from tests.test_gpu_decoder import make_cache, run_attention, sees_of, trees, words_of
 from tests.test_gpu_prompts import BF16, check_attention4, check_prompt, make_cache4, offsets, run_attention4, run_prompt
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,77 @@ def test_scales_whose_logarithm_leaves_the_range(ctx):
     kn, vn, sees = (t[None, :2] for t in (k, v, torch.ones(2, 2, dtype=torch.bool).tril()))
     out = run_attention4(ctx, q[None, :2], parts, kn, vn, None, table, [20], 2.0 ** 127)
     check_attention4(out, q[None, :2], parts, kn, vn, sees, table, [20], 2.0 ** 127)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+@pytest.mark.parametrize("n,held", [(300, 0), (40, 3000)])
+def test_unlike_weights_of_the_largest_value(ctx, dtype, n, held):
+    """Values that are all the largest one have it as their mean: the weights' rounding may take half a step off it, not
+    past it."""
+    top = torch.finfo(dtype).max
+    g = torch.Generator().manual_seed(37)
+    q, k = torch.randn(n, 4, 64, generator=g).to(dtype), torch.randn(n + held, 2, 64, generator=g).to(dtype)
+    v = torch.full_like(k, top)
+    v[:, 1] = -top
+    cu_q, cu_k = [0, n], [0, n + held]
+    out = run_prompt(ctx, q, k, v, cu_q, cu_k, 0.3)
+    assert out.isfinite().all()
+    check_prompt(out, q, k, v, cu_q, cu_k, 0.3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+@pytest.mark.parametrize("N,G,lens", [(20, 1, [0, 0]), (64, 2, [0, 0]), (64, 8, [0, 0])])
+def test_unlike_weights_of_the_largest_new_value_over_4_bits(ctx, dtype, N, G, lens):
+    D, B = 64, len(lens)
+    g = torch.Generator().manual_seed(38)
+    parts, table = make_cache4(lens, N, 2, D, 16, 39, dtype=dtype)
+    q, kn = torch.randn(B, N, 2 * G, D, generator=g).to(dtype), torch.randn(B, N, 2, D, generator=g).to(dtype)
+    vn = torch.full_like(kn, torch.finfo(dtype).max)
+    vn[:, :, 1] *= -1
+    sees = sees_of(trees(random.Random(5), B, N, 0))
+    out = run_attention4(ctx, q, parts, kn, vn, None, table, lens, 0.3)
+    assert out.isfinite().all()
+    check_attention4(out, q, parts, kn, vn, sees, table, lens, 0.3)
+
+
+def rounded_up(dtype):
+    """A scale at which a score of -1 weighs a little over half of a step above 0.5, so that the type rounds it up: by
+    nearly a relative 2^-11 in fp16 and 2^-8 in bf16. The largest number is half of that away from an infinity."""
+    step = torch.finfo(dtype).eps  # of numbers from 1 to 2
+    return -math.log(0.5 * (1 + 0.55 * step))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+@pytest.mark.parametrize("held", [199, 3999])
+def test_weights_rounded_up_of_the_largest_value(ctx, dtype, held):
+    """One key of weight 1 and many of a weight that is rounded up, all of the largest value."""
+    k = torch.zeros(1 + held, 1, 64, dtype=dtype)
+    k[1:, :, 0] = -1
+    q, v = torch.zeros(1, 2, 64, dtype=dtype), torch.full_like(k, torch.finfo(dtype).max)
+    q[:, :, 0] = 1
+    out = run_prompt(ctx, q, k, v, [0, 1], [0, 1 + held], rounded_up(dtype))
+    assert (out == torch.finfo(dtype).max).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+@pytest.mark.parametrize("N,G", [(32, 1), (64, 2), (64, 8)])
+def test_weights_rounded_up_of_the_largest_new_value_over_4_bits(ctx, dtype, N, G):
+    parts, table = make_cache4([0], N, 1, 64, 16, 40, dtype=dtype)
+    kn, q = torch.zeros(1, N, 1, 64, dtype=dtype), torch.zeros(1, N, G, 64, dtype=dtype)
+    kn[:, 1:, :, 0], q[..., 0] = -1, 1
+    vn = torch.full_like(kn, -torch.finfo(dtype).max)
+    out = run_attention4(ctx, q, parts, kn, vn, None, table, [0], rounded_up(dtype))
+    assert (out == -torch.finfo(dtype).max).all()
+
+
+@pytest.mark.parametrize("N,G,n", [(32, 1, 0), (64, 2, 0), (64, 8, 0), (1, 1, 2000)])
+def test_weights_rounded_up_of_the_largest_value_over_a_plain_cache(ctx, N, G, n):
+    dtype = torch.float16
+    k, v, table = make_cache(ctx, [n], n + N, 1, 64, 16, dtype, 41)
+    k.zero_()
+    k[..., 0] = -1
+    kn, q = torch.zeros(1, N, 1, 64, dtype=dtype), torch.zeros(1, N, G, 64, dtype=dtype)
+    kn[:, 1:, :, 0], q[..., 0] = -1, 1
+    v, vn = (torch.full_like(t, torch.finfo(dtype).max) for t in (v, kn))
+    out = run_attention(ctx, q, k, v, kn, vn, None, table, [n], rounded_up(dtype))
+    assert (out == torch.finfo(dtype).max).all()
