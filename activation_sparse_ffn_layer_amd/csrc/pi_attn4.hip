@@ -58,8 +58,9 @@ __device__ __forceinline__ void put_codes(uint8_t* p, u32x4 codes, uint16_t scal
 }
 
 // The exact fp16 form of a query's fragments (the value that scale_c then takes off): bf16 queries times the
-// power of two that brings the row's largest element into [2^14, 2^15). Elements 2^28 times smaller
-// may be subnormal in fp16; they are lost beside the row's rounding.
+// power of two that brings the row's largest element into [2^14, 2^15). Elements more than 2^31 times smaller lose bits in
+// fp16, more than 2^39 times smaller ones are zeros: where the largest meets keys of its own size, that is far below the
+// score's rounding in fp32; where it meets zeros, it is a limit of the operator.
 __device__ __forceinline__ float rows_max(float v);
 template <bool QUARTERS, int KS>  // a row's elements are in four lanes, not two
 __device__ __forceinline__ float queries_to_half(u32x4 (&qf)[KS]) {
@@ -160,7 +161,8 @@ template <int DP> constexpr size_t attn4_lds() { return 2 * (size_t)KT4 * (k_pit
 
 // WQ waves of 32 query rows each; tiles of 64 keys in LDS, which all waves read: a tile is turned into fp16 once for all of
 // them. Bound by products, exponentials and that conversion in turn: 26 nodes of 4 sequences (up to 32768 positions, 64
-// heads, 8 kv, of 128, 90 GFLOP; 208 of 256 rows in use) 153 to 173 us. Four waves for all: 182; twice as many spans: 190.
+// heads, 8 kv, of 128, 90 GFLOP; 208 of 256 rows in use) 153 to 173 us, of 64 102; up to 16384 positions, 32 heads (8 kv) of
+// 256, whose registers spill, 202 in fp16 and 304 in bf16. Four waves for all: 182; twice as many spans: 190.
 template <typename T, int DP, int WQ>
 __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tree_attn4(AttnDev a, Kv4Dev sc) {
   constexpr int KB = 2, KT = KT4, NT = 64 * WQ, KS = DP / 16, DB = DP / 32;
@@ -437,7 +439,9 @@ __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // from memory through registers straight into the products; values pass through LDS of the wave's own,
 // where they are transposed. No barrier is in the loop. FULL: heads fill the padded size.
 // One token of 64 sequences (8191 positions, 64 heads, 8 kv, of 128; 430 MB): 101 to 113 us, of which the loads alone take
-// 97 and the rest alone 60. One token over 512 positions of 32 heads: 11 us, three dependent loads and the join's launch.
+// 97 and the rest alone 60; 149 where pages of 5 tokens hold a token's heads side by side. Heads of 32 and of 64: 67 us (of
+// 32 half of each wave's lanes hold a block twice), of 96: 96; 32 sequences of heads of 256, whose registers spill: 151. One
+// token over 512 positions of 32 heads: 11 us, three dependent loads and the join's launch.
 // Workgroups a CU holds (waves per SIMD), and tiles in flight: three with one tile ahead where the registers allow it, 112
 // against 118 us with two of two tiles (one token of 64 sequences).
 constexpr int few_wgs(int DP, int rows) { return DP > 128 ? (rows > 16 ? 1 : 2) : rows > 16 ? 2 : 3; }

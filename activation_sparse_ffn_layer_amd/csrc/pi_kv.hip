@@ -48,9 +48,9 @@ __global__ __launch_bounds__(BLOCK) void k_kv_append(AppendDev p) {
 // so are the halves of its code bytes (elements j and j + 16 are two lanes apart). scale = -m/8 rounded to 8
 // significant bits: times a code it is an fp16 number exactly. The quotient by the scale: its product with the rounded
 // reciprocal lands off a tie; corrected by that product's remainder, which is exact, it is the rounded quotient
-// (Markstein). Bound by the quantiser's arithmetic, about 130 instructions for 8
-// elements, next to chains of
-// dependent loads: 16 x 1024 tokens of 8 heads of 128 (86 MB) 26 us, 3.3 TB/s; 16 short paths 3.8 us, latency.
+// (Markstein). 16 x 1024 tokens of 8 heads of 128 (86 MB) 26 us, 3.3 TB/s: the quantiser's arithmetic, about 130
+// instructions for 8 elements, is 14 of them, next to dependent loads (a token's place, then a row for each of a lane's
+// items, waited for where it is converted). 16 short paths 3.8 us, latency.
 constexpr int KV_ROWS = 16;  // rows of a workgroup, at most
 // The value of a lane of the same four: 0xB1 the neighbour's, 0x4E that two on.
 template <int CTRL, typename V>
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(BLOCK) void k_kv4_append(AppendDev p, Kv4Dev sc, Pa
   }
   __syncthreads();
   const int each = p.HK * p.pieces;  // a multiple of 4: the lanes of a block go together
-  constexpr int U = 2;               // items of a lane in flight
+  constexpr int U = 2;               // items of a lane a round
   for (int i0 = threadIdx.x; i0 < rows * 2 * each; i0 += U * BLOCK) {
     float x[U][8];
     int row[U], h[U];
@@ -160,9 +160,9 @@ struct ReadDev {
 
 // Rows from the cache, `per` consecutive ones a workgroup: it counts the sequences that start at or before
 // its first row, and each row steps on from there. Bound by memory:
-// 131072 rows of 8 heads of 128 from 4 bits, 497 MB, 100 us, 5.0 TB/s. An item is 16 bytes put out, so that
-// a wave's stores are whole lines; of a 4-bit row it is one half of 8 code bytes (written as both halves, 32 bytes each
-// of a line in two stores, 131072 rows of 8 heads of 128 took 141 us).
+// 94745 rows (8 sequences of up to 16384) of 8 heads of 128 from 4 bits, 497 MB, 98 to 106 us, 4.7 to 5.1 TB/s; from a plain
+// cache, 776 MB, 155 us, 5.0 TB/s. An item is 16 bytes put out, so that a wave's stores are whole lines; of a 4-bit row it is
+// one half of 8 code bytes (written as both halves, 32 bytes each of a line in two stores, the same rows took 141 us).
 template <typename T, bool Q4>
 __global__ __launch_bounds__(BLOCK) void k_kv_read(ReadDev p) {
   __shared__ long long s_page[KV_ROWS];  // page number, or -1: zeros, -2: the row stays
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(BLOCK) void k_kv_read(ReadDev p) {
       } else if (!held[u]) {
         w4[u] = (u32x4){0, 0, 0, 0};
       }
-      // past the caches' usual order: 127 -> 103 us for 131072 rows of 8 heads of 128
+      // past the caches' usual order: 127 -> 103 us for 94745 rows of 8 heads of 128
       __builtin_nontemporal_store(w4[u], reinterpret_cast<u32x4*>(o[u]));
     }
   }

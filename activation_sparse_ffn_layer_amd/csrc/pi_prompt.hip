@@ -8,9 +8,11 @@
 // that it reads a key once for all of them and little of the diagonal's tiles is masked.
 //
 // Bound by the products and the weights' vector work at a clock that gives way to power: 16384 tokens of 32 heads (8 kv) of
-// 128 in bf16, 2199 GFLOP, 2118 us, 1038 TFLOP/s (a large library product: 1280 to 1360; with zeros as data 1840 us). 16
-// packed sequences of up to 2047 tokens and 1500 held, 64 heads, 1335 us: each workgroup starts with some 4 us of
-// dependent loads. 500 tokens: 21 us, up to 8 tiles one after another.
+// 128 in bf16, 2199 GFLOP, 2163 to 2249 us, 0.98 to 1.02 PFLOP/s (a large library product: 1.28 to 1.42; the first calls after
+// a pause 2320 to 2630 us; with zeros as data 1862). 8192 tokens of 32 heads (8 kv) of 64, 80, 96: 382, 465, 475 us (0.72,
+// 0.74, 0.87); of 16 heads (8 kv) of 256, whose registers spill: 1620 (0.34). 16 packed sequences of up to 2047 tokens and
+// 1500 held, 64 heads, 1353 to 1403 us: each workgroup starts with some 4 us of dependent loads, with nothing beside it on
+// its CU. 500 tokens: 20 to 21 us, up to 8 tiles one after another.
 #include <algorithm>
 #include <new>
 
@@ -79,7 +81,6 @@ __device__ __forceinline__ int packed(const int32_t* cu, int b, int rows, int* f
 }
 
 template <int DP> constexpr size_t prompt_lds() { return 2 * (size_t)PKT * (k_pitch<DP>() + v_pitch<DP>()); }
-constexpr int padded_dim_p(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 
 template <typename T, int DP, int WQ>
 __global__ __launch_bounds__(64 * WQ) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_prompt(PromptDev a) {
@@ -415,7 +416,7 @@ pi_status launch_prompt_d(pi_ctx* c, const PromptDev& a, int wq) {
 
 template <typename T>
 pi_status launch_prompt(pi_ctx* c, const PromptDev& a, int wq) {
-  switch (padded_dim_p(a.D)) {
+  switch (padded_dim(a.D)) {
     case 64: return launch_prompt_d<T, 64>(c, a, wq);
     case 96: return launch_prompt_d<T, 96>(c, a, wq);
     case 128: return launch_prompt_d<T, 128>(c, a, wq);
@@ -443,7 +444,7 @@ pi_status pi_prompt_create(pi_ctx* ctx, int32_t dtype, int32_t heads, int32_t kv
   if (((int64_t)max_tokens + 256ll * max_batch) * heads >= 1ll << 29)
     return fail(ctx, PI_ERR_UNSUPPORTED, "%d tokens of %d sequences and %d heads are too many", max_tokens, max_batch, heads);
   // scratch of the largest call whose keys are split, of however many rows
-  const int HK = kv_heads, G = heads / kv_heads, DP = padded_dim_p(head_dim);
+  const int HK = kv_heads, G = heads / kv_heads, DP = padded_dim(head_dim);
   size_t rows = 0;
   for (int64_t n = 1; n <= max_tokens; n += std::max<int64_t>(1, n / 64)) {
     const int64_t next = std::min<int64_t>(max_tokens, n + std::max<int64_t>(1, n / 64) - 1);
@@ -495,7 +496,7 @@ pi_status pi_prompt_attention(pi_ctx* ctx, pi_prompt* prompt, const pi_prompt_ar
     PI_TRY(check_bnh(ctx, "v", a.v, 0, a.v_row, a.v_head));
   }
   PI_HIP(ctx, hipSetDevice(ctx->device));
-  const int HK = prompt->kv_heads, G = prompt->heads / HK, DP = padded_dim_p(prompt->head_dim);
+  const int HK = prompt->kv_heads, G = prompt->heads / HK, DP = padded_dim(prompt->head_dim);
   PromptPlan p = prompt_plan(ctx->cus, HK, G, DP, a.q_rows, a.B, a.k_rows);
   const int64_t rows = (int64_t)a.q_rows * prompt->heads;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.splits, (int64_t)prompt->ws_rows / rows));

@@ -1,12 +1,15 @@
 // RMS norm of query and key heads with rotary positions (pi_qk_norm_rope).
 //
 // y = x / sqrt(mean(x^2) + eps) * w per head, then each pair (a, b) of the first rot elements turns by
-// pos * inv_freq: (a cos - b sin, b cos + a sin). Bound by memory: a head is read once, kept in
-// registers and written once. A workgroup takes up to ROPE_TOKENS tokens; it works their sines and cosines out first, one
-// angle a thread, into LDS. A lane then has the same 2U elements of every head it takes (U pairs: two pieces of U elements
-// each, U * i and rot/2 + U * i, or 2U in a row where pairs are interleaved), HEADS_AHEAD heads in flight.
-// 8192 tokens of 72 heads of 128 in bf16 with norms, 302 MB: 62 us, 4.8 TB/s, near a copy's rate (four heads in flight 70,
-// one 65; with every wave working its sines out itself 89). 8 tokens: 4 us, latency.
+// pos * inv_freq: (a cos - b sin, b cos + a sin). A head is read once and written once. A workgroup takes up to ROPE_TOKENS
+// tokens; it works their sines and cosines out first, one angle a thread, into LDS. A lane then has the same 2U elements of
+// every head it takes (U pairs: two pieces of U elements each, U * i and rot/2 + U * i, or 2U in a row where pairs are
+// interleaved), HEADS_ROUND heads a round. As compiled, a head's rows are waited for before the next head's are asked for:
+// their conversion to fp32 stands in the branch of the lanes that have a head. But for bf16 in pieces of 8 elements one
+// element of each piece also passes through scratch memory (20 to 80 bytes a lane).
+// With norms, 302 MB: 8192 tokens of 72 heads of 128 in bf16 62 us, 4.9 TB/s, near a copy's rate (four heads a round 70, one
+// 65; with every wave working its sines out itself 89); in fp16 84 us; 4096 such tokens in fp32 126 us. 151 MB in bf16, 40
+// heads of 64, of 256, or of 128 half turned: 30 us; of 80: 35. 8 tokens: 4 us, latency.
 //
 // The angle is a whole number times an fp32 number, exact in 64 bits up to 2^29 and off by 2^-53 of
 // itself beyond; as turns, reduced by its nearest whole number, it goes on in fp32 (2^-25 of a turn).
@@ -105,7 +108,7 @@ __device__ __forceinline__ void normalise(const RopeDev& p, const RopeSide& side
   }
 }
 
-constexpr int ROPE_TOKENS = 8, HEADS_AHEAD = 2;
+constexpr int ROPE_TOKENS = 8, HEADS_ROUND = 2;
 
 // LPH lanes per head, a power of two. Heads are numbered token by token, queries first, then keys.
 template <typename TX, typename TY, int U, bool PAIRS, int LPH>
@@ -126,12 +129,12 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
   if (!live) a0 = b0 = 0;
   const int total = p.heads + p.kv_heads;
   const int first = blockIdx.y * p.part + threadIdx.x / LPH, end = min((int)(blockIdx.y + 1) * p.part, tokens * total);
-  float a[HEADS_AHEAD][U], b[HEADS_AHEAD][U];
-  int tok[HEADS_AHEAD], head[HEADS_AHEAD];
-  bool in[HEADS_AHEAD], key[HEADS_AHEAD];
+  float a[HEADS_ROUND][U], b[HEADS_ROUND][U];
+  int tok[HEADS_ROUND], head[HEADS_ROUND];
+  bool in[HEADS_ROUND], key[HEADS_ROUND];
   auto load = [&](int h0) {
 #pragma unroll
-    for (int n = 0; n < HEADS_AHEAD; ++n) {
+    for (int n = 0; n < HEADS_ROUND; ++n) {
       const int h = h0 + n * HPB;
       in[n] = live && h < end;
       uint32_t hh;
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
       }
     }
   };
-  load(first);  // before the angles, whose arithmetic takes as long
+  load(first);  // the rows are converted before the angles' loads
   for (int i = threadIdx.x; i < tokens * half; i += BLOCK) {
     const int t = i / half, k = i - t * half;
     const double turns = (double)p.pos[t0 + t] * (double)p.inv_freq[k] * 0.15915494309189533577;  // 1 / (2 pi)
@@ -159,10 +162,10 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
     turn[(2 * t + 1) * half + k] = s;
   }
   __syncthreads();
-  for (int h0 = first; h0 - (int)threadIdx.x / LPH < end; h0 += HEADS_AHEAD * HPB) {
+  for (int h0 = first; h0 - (int)threadIdx.x / LPH < end; h0 += HEADS_ROUND * HPB) {
     if (h0 != first) load(h0);
 #pragma unroll
-    for (int n = 0; n < HEADS_AHEAD; ++n) {
+    for (int n = 0; n < HEADS_ROUND; ++n) {
       const RopeSide& side = key[n] ? p.k : p.q;
       if (p.q.w != nullptr || p.k.w != nullptr) normalise<U, LPH>(p, side, a0, b0, a[n], b[n]);
       if (!in[n]) continue;
@@ -203,10 +206,10 @@ template <typename TX, typename TY, int U, bool PAIRS, int LPH>
 pi_status launch_rope(pi_ctx* c, RopeDev p, int T) {
   constexpr int HPB = BLOCK / LPH;
   const int total = p.heads + p.kv_heads;
-  // As many tokens as leave 4 workgroups for each CU, and no more than heads in flight need; then, where there are few
+  // As many tokens as leave 4 workgroups for each CU, and no more than two rounds of heads need; then, where there are few
   // tokens, their heads in parts of as many as a workgroup has lanes for.
-  p.tokens = std::max(1, std::min({ROPE_TOKENS, T / (4 * c->cus), (HEADS_AHEAD * HPB * 2 + total - 1) / total}));
-  p.part = p.tokens > 1 ? p.tokens * total : HEADS_AHEAD * HPB;
+  p.tokens = std::max(1, std::min({ROPE_TOKENS, T / (4 * c->cus), (HEADS_ROUND * HPB * 2 + total - 1) / total}));
+  p.part = p.tokens > 1 ? p.tokens * total : HEADS_ROUND * HPB;
   p.by_heads = page_div(total);
   const dim3 grid((T - 1) / p.tokens + 1, (p.tokens * total - 1) / p.part + 1);
   PI_HIP(c, launch_k(c, 0, k_qk_norm_rope<TX, TY, U, PAIRS, LPH>, grid, p.tokens * p.rot * sizeof(float), p));

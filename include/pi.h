@@ -402,7 +402,9 @@ pi_status pi_kv_read(pi_ctx *ctx, const pi_kv *kv, const pi_read_args *args);
  *   out[b][i][h] = sum_p w_p v_p,  w = softmax over the seen p of scale * q[b][i][h] . k_p,
  * with key/value head h * kv_heads / heads. A node that sees nothing gets zeros; what is not
  * seen does not enter the result, whatever it holds. Over a 4-bit cache the cached keys and values are its
- * values, the new nodes' are given in its dtype.
+ * values, the new nodes' are given in its dtype; of a bf16 query, elements more than 2^31 times smaller than the
+ * head's largest lose bits there, more than 2^39 times smaller ones count as zeros. Sums are in fp32: over a plain
+ * bf16 cache, values above 2^128 / (ctx_len + N) may leave its range.
  *   heads      query heads, a multiple of the cache's heads
  *   scale      above 0, at most 2^127
  *   max_batch, max_nodes (1..64)   limits of B and N, which size the scratch
@@ -559,7 +561,8 @@ typedef struct pi_prompt_args {
 pi_status pi_prompt_attention(pi_ctx *ctx, pi_prompt *prompt, const pi_prompt_args *args);
 
 /* RMS norm of every query and key head, and rotary positions, in one pass over T tokens:
- *   y = x / sqrt(mean(x^2) + eps) * w      per head of head_dim elements (y = x without w)
+ *   y = x / sqrt(mean(x^2) + eps) * w      per head of head_dim elements (y = x without w; zeros
+ *                                          for a head of zeros where eps is 0)
  *   out = y with pair i of its first `rot` elements turned by the angle pos[t] * inv_freq[i]:
  *         (a, b) becomes (a cos - b sin, b cos + a sin)
  * Pair i is elements i and i + rot/2, or 2i and 2i + 1 where `interleaved`. Angles are formed and
