@@ -81,7 +81,7 @@ __global__ __launch_bounds__(BLOCK) void k_kv4_append(AppendDev p, Kv4Dev sc, Pa
   }
   __syncthreads();
   const int each = p.HK * p.pieces;  // a multiple of 4: the lanes of a block go together
-  constexpr int U = 2;               // items of a lane a round
+  constexpr int U = 2;               // items of a lane a step
   for (int i0 = threadIdx.x; i0 < rows * 2 * each; i0 += U * BLOCK) {
     float x[U][8];
     int row[U], h[U];

@@ -4,10 +4,10 @@
 // pos * inv_freq: (a cos - b sin, b cos + a sin). A head is read once and written once. A workgroup takes up to ROPE_TOKENS
 // tokens; it works their sines and cosines out first, one angle a thread, into LDS. A lane then has the same 2U elements of
 // every head it takes (U pairs: two pieces of U elements each, U * i and rot/2 + U * i, or 2U in a row where pairs are
-// interleaved), HEADS_ROUND heads a round. As compiled, a head's rows are waited for before the next head's are asked for:
+// interleaved), HEADS_STEP heads a step. As compiled, a head's rows are waited for before the next head's are asked for:
 // their conversion to fp32 stands in the branch of the lanes that have a head. But for bf16 in pieces of 8 elements one
 // element of each piece also passes through scratch memory (20 to 80 bytes a lane).
-// With norms, 302 MB: 8192 tokens of 72 heads of 128 in bf16 62 us, 4.9 TB/s, near a copy's rate (four heads a round 70, one
+// With norms, 302 MB: 8192 tokens of 72 heads of 128 in bf16 62 us, 4.9 TB/s, near a copy's rate (four heads a step 70, one
 // 65; with every wave working its sines out itself 89); in fp16 84 us; 4096 such tokens in fp32 126 us. 151 MB in bf16, 40
 // heads of 64, of 256, or of 128 half turned: 30 us; of 80: 35. 8 tokens: 4 us, latency.
 //
@@ -108,7 +108,7 @@ __device__ __forceinline__ void normalise(const RopeDev& p, const RopeSide& side
   }
 }
 
-constexpr int ROPE_TOKENS = 8, HEADS_ROUND = 2;
+constexpr int ROPE_TOKENS = 8, HEADS_STEP = 2;
 
 // LPH lanes per head, a power of two. Heads are numbered token by token, queries first, then keys.
 template <typename TX, typename TY, int U, bool PAIRS, int LPH>
@@ -129,12 +129,12 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
   if (!live) a0 = b0 = 0;
   const int total = p.heads + p.kv_heads;
   const int first = blockIdx.y * p.part + threadIdx.x / LPH, end = min((int)(blockIdx.y + 1) * p.part, tokens * total);
-  float a[HEADS_ROUND][U], b[HEADS_ROUND][U];
-  int tok[HEADS_ROUND], head[HEADS_ROUND];
-  bool in[HEADS_ROUND], key[HEADS_ROUND];
+  float a[HEADS_STEP][U], b[HEADS_STEP][U];
+  int tok[HEADS_STEP], head[HEADS_STEP];
+  bool in[HEADS_STEP], key[HEADS_STEP];
   auto load = [&](int h0) {
 #pragma unroll
-    for (int n = 0; n < HEADS_ROUND; ++n) {
+    for (int n = 0; n < HEADS_STEP; ++n) {
       const int h = h0 + n * HPB;
       in[n] = live && h < end;
       uint32_t hh;
@@ -162,10 +162,10 @@ __global__ __launch_bounds__(BLOCK) void k_qk_norm_rope(RopeDev p) {
     turn[(2 * t + 1) * half + k] = s;
   }
   __syncthreads();
-  for (int h0 = first; h0 - (int)threadIdx.x / LPH < end; h0 += HEADS_ROUND * HPB) {
+  for (int h0 = first; h0 - (int)threadIdx.x / LPH < end; h0 += HEADS_STEP * HPB) {
     if (h0 != first) load(h0);
 #pragma unroll
-    for (int n = 0; n < HEADS_ROUND; ++n) {
+    for (int n = 0; n < HEADS_STEP; ++n) {
       const RopeSide& side = key[n] ? p.k : p.q;
       if (p.q.w != nullptr || p.k.w != nullptr) normalise<U, LPH>(p, side, a0, b0, a[n], b[n]);
       if (!in[n]) continue;
@@ -206,10 +206,10 @@ template <typename TX, typename TY, int U, bool PAIRS, int LPH>
 pi_status launch_rope(pi_ctx* c, RopeDev p, int T) {
   constexpr int HPB = BLOCK / LPH;
   const int total = p.heads + p.kv_heads;
-  // As many tokens as leave 4 workgroups for each CU, and no more than two rounds of heads need; then, where there are few
+  // As many tokens as leave 4 workgroups for each CU, and no more than two steps of heads need; then, where there are few
   // tokens, their heads in parts of as many as a workgroup has lanes for.
-  p.tokens = std::max(1, std::min({ROPE_TOKENS, T / (4 * c->cus), (HEADS_ROUND * HPB * 2 + total - 1) / total}));
-  p.part = p.tokens > 1 ? p.tokens * total : HEADS_ROUND * HPB;
+  p.tokens = std::max(1, std::min({ROPE_TOKENS, T / (4 * c->cus), (HEADS_STEP * HPB * 2 + total - 1) / total}));
+  p.part = p.tokens > 1 ? p.tokens * total : HEADS_STEP * HPB;
   p.by_heads = page_div(total);
   const dim3 grid((T - 1) / p.tokens + 1, (p.tokens * total - 1) / p.part + 1);
   PI_HIP(c, launch_k(c, 0, k_qk_norm_rope<TX, TY, U, PAIRS, LPH>, grid, p.tokens * p.rot * sizeof(float), p));

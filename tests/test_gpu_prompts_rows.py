@@ -165,7 +165,7 @@ def test_memory_of_a_busy_stream_is_not_reused():
         torch.cuda.synchronize()
         if busy:
             with torch.cuda.stream(st):
-                for _ in range(60):
+                for _ in range(200):
                     torch.mm(a, a, out=b)
         pi.qk_norm_rope(c, t["q"], t["k"], t["pos"], t["freq"], qr, kr, q_norm=t["w"])
         pi.prompt_attention(c, prompt, t["q"], t["k"], t["v"], t["cu"], None, o)
